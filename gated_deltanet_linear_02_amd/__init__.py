@@ -19,11 +19,18 @@ Entry points (same names as the C ABI, without the ``gdn_`` prefix):
     tune_prefill(q, k, v, g, beta, cu_seqlens, ...) -> chosen method, per-candidate
         times and gate errors (cached for prefill's chunk 0);
     tune_cache_clear / tune_cache_size / tune_cache_save / tune_cache_load
+    linattn_prefill(q, k, v, g, cu_seqlens, ...) -> (out, final_state)
+    linattn_decode_step(q, k, v, g, state, ...)  -> out
+        linear attention with a decay per head: S = exp(g) S + v k^T
+    linattn_prefill_workspace_size(...)
+    state_cache_write(state, cache, scales, ...) /
+    state_cache_read(cache, scales, state, ...)  -> states kept at 8 bits
     timing_start(max_launches) / timing_stop()  -> per-kernel launch times
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -35,6 +42,8 @@ __all__ = [
     "GdnError", "lib_path", "load", "prefill", "prefill_noalloc", "decode_step", "prefill_workspace_size", "prefill_method",
     "prefill_plan", "tune_prefill", "method_name", "TUNE_CANDIDATES", "tune_cache_clear", "tune_cache_size",
     "tune_cache_save", "tune_cache_load", "timing_start", "timing_stop", "abi_version", "KERNEL_KINDS",
+    "linattn_prefill", "linattn_prefill_workspace_size", "linattn_decode_step", "state_cache_write",
+    "state_cache_read",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -43,7 +52,8 @@ _lib = None
 _lock = threading.Lock()
 
 GDN_BF16, GDN_F32 = 0, 1
-KERNEL_KINDS = ("schedule", "prep", "scan", "decode", "token_scan", "decode_norm", "norm_apply")
+KERNEL_KINDS = ("schedule", "prep", "scan", "decode", "token_scan", "decode_norm", "norm_apply",
+                "linattn_state", "linattn_join", "linattn_out", "linattn_decode", "cache_write", "cache_read")
 
 STATUS = {
     0: "GDN_OK", 1: "GDN_ERR_NULL_ARG", 2: "GDN_ERR_BAD_SHAPE", 3: "GDN_ERR_UNSUPPORTED",
@@ -117,6 +127,18 @@ def load():
         L.gdn_tune_cache_save.argtypes = [ctypes.c_char_p]
         L.gdn_tune_cache_load.restype = i32
         L.gdn_tune_cache_load.argtypes = [ctypes.c_char_p, ctypes.POINTER(i32)]
+        L.gdn_linattn_prefill_workspace_size.restype = sz
+        L.gdn_linattn_prefill_workspace_size.argtypes = [i32, i64, i64, i32, i32, i32, i32, i32]
+        L.gdn_linattn_prefill.restype = i32
+        L.gdn_linattn_prefill.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i32, i32, i32, i32, f32, i32, i32,
+                                          i32, vp, vp, i32, vp, vp, sz, vp]
+        L.gdn_linattn_decode_step.restype = i32
+        L.gdn_linattn_decode_step.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, i32, vp, vp,
+                                              i32, vp, i32, vp, vp]
+        L.gdn_state_cache_write.restype = i32
+        L.gdn_state_cache_write.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp]
+        L.gdn_state_cache_read.restype = i32
+        L.gdn_state_cache_read.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, vp]
         L.gdn_timing_start.restype = i32
         L.gdn_timing_start.argtypes = [i32]
         L.gdn_timing_stop.restype = i32
@@ -362,6 +384,183 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
             _stream(q.device, stream))
     _check(status)
     return out
+
+
+@contextlib.contextmanager
+def _on_stream(device: torch.device, stream):
+    """The call's device made current (the null stream means the current
+    device's), and its stream torch's current one, so that what is allocated
+    for the call belongs to the stream that uses it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device)
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _indices(name: str, t: Optional[torch.Tensor], n: int) -> None:
+    _expect(name, t, (n,))
+    if t is not None and t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+
+
+def _state_dtype(name: str, t: torch.Tensor) -> None:
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _linattn_inputs(q, k, v, g) -> Tuple[int, int, int, int, int, int]:
+    """Shapes and types that both linear-attention calls share; (rows, hk,
+    hv, dk, dv, 1 if g is one gate per head)."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must be [tokens, heads, size]")
+    n, hk, dk = q.shape
+    hv, dv = v.shape[1], v.shape[2]
+    _expect("k", k, (n, hk, dk), q.dtype)
+    _expect("v", v, (n, hv, dv), q.dtype)
+    per_head = g.dim() == 1
+    _expect("g", g, (hv,) if per_head else (n, hv))
+    return n, hk, hv, dk, dv, int(per_head)
+
+
+def linattn_prefill_workspace_size(num_seqs: int, total_tokens: int, hk: int, hv: int, dk: int, dv: int,
+                                   io_dtype: torch.dtype = torch.bfloat16,
+                                   max_seqlen: Optional[int] = None) -> int:
+    """Bytes of workspace that ``linattn_prefill`` needs for these sizes; 256
+    where it needs none, 0 if the sizes are rejected."""
+    return int(load().gdn_linattn_prefill_workspace_size(num_seqs, total_tokens, int(max_seqlen or 0), hk, hv, dk,
+                                                         dv, _dtype_code(io_dtype)))
+
+
+def linattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                    *, scale: float = 1.0, initial_state: Optional[torch.Tensor] = None,
+                    final_state: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, write_final_state: bool = True,
+                    state_dtype: Optional[torch.dtype] = None, max_seqlen: Optional[int] = None,
+                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay per head over packed sequences
+    (``gdn_linattn_prefill``): S = exp(g) S + v k^T, o = scale S q.
+
+    q, k [T, hk, dk]; v [T, hv, dv] (bf16 or fp32, one dtype); g [T, hv], or
+    [hv] for one gate per head (bf16 or fp32); cu_seqlens int32 [N + 1] on the
+    device; states [N, hv, dv, dk], fp32 or (bf16 I/O) bf16: the dtype of the
+    state tensors given, else ``state_dtype`` (default fp32).
+    ``final_state`` may be ``initial_state`` (in place). ``max_seqlen`` (host
+    int, or None): the longest sequence's length, which steers how the work is
+    split. Missing out / final_state / workspace are allocated with torch.
+    Returns (out, final_state). No gradient is recorded.
+    """
+    T, hk, hv, dk, dv, per_head = _linattn_inputs(q, k, v, g)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+        raise TypeError("cu_seqlens must be a 1-d int32 tensor")
+    N = cu_seqlens.numel() - 1
+    io, gate = _dtype_code(q.dtype), _dtype_code(g.dtype)
+    _expect("out", out, (T, hv, dv), q.dtype)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        _expect(name, t, (N, hv, dv, dk))
+    given = {t.dtype for t in (initial_state, final_state) if t is not None}
+    if len(given) > 1:
+        raise TypeError("initial_state and final_state must have one dtype")
+    sdt = given.pop() if given else (state_dtype or torch.float32)
+    if state_dtype is not None and sdt != state_dtype:
+        raise TypeError(f"state tensors are {sdt}, state_dtype says {state_dtype}")
+    hint = int(max_seqlen or 0)
+    dev = q.device
+    _on_device(dev, q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state,
+               final_state=final_state, out=out, workspace=workspace)
+    with _on_stream(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, hv, dv), dtype=q.dtype, device=dev)
+        if final_state is None and write_final_state:
+            final_state = torch.empty((N, hv, dv, dk), dtype=sdt, device=dev)
+        if workspace is None:
+            need = linattn_prefill_workspace_size(N, T, hk, hv, dk, dv, q.dtype, hint)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 256 else None
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(load().gdn_linattn_prefill(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, hint, hk, hv, dk, dv, float(scale), io,
+            gate, per_head, _ptr(initial_state), _ptr(final_state), _dtype_code(sdt), _ptr(out), _ptr(workspace),
+            ws_bytes, st.cuda_stream or None))
+    return out, final_state
+
+
+def linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *,
+                        scale: float = 1.0, state_slots: Optional[torch.Tensor] = None,
+                        state_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """One token per sequence of the linear attention with a decay per head
+    (``gdn_linattn_decode_step``). q, k [B, hk, dk]; v [B, hv, dv]; g [B, hv]
+    or [hv]; state [slots, hv, dv, dk], fp32 or (bf16 I/O) bf16; state_slots
+    int32 [B] on the device or None. The states are updated in place, or, with
+    ``state_out`` (a second pool like ``state``), written to the same slots
+    there while ``state`` stays as it is. No gradient is recorded."""
+    B, hk, hv, dk, dv, per_head = _linattn_inputs(q, k, v, g)
+    _state_dtype("state", state)
+    _expect("state", state, (state.shape[0], hv, dv, dk))
+    _expect("state_out", state_out, tuple(state.shape), state.dtype)
+    _expect("out", out, (B, hv, dv), q.dtype)
+    _indices("state_slots", state_slots, B)
+    dev = q.device
+    _on_device(dev, q=q, k=k, v=v, g=g, state=state, state_out=state_out, state_slots=state_slots, out=out)
+    with _on_stream(dev, stream) as st:
+        if out is None:
+            out = torch.empty((B, hv, dv), dtype=q.dtype, device=dev)
+        _check(load().gdn_linattn_decode_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), B, hk, hv, dk, dv, float(scale), _dtype_code(q.dtype),
+            _dtype_code(g.dtype), per_head, _ptr(state), _ptr(state_out), _dtype_code(state.dtype),
+            _ptr(state_slots), state.shape[0], _ptr(out), st.cuda_stream or None))
+    return out
+
+
+GDN_I8, GDN_E4M3 = 0, 1
+
+
+def _state_cache(state, cache, scales, slots, entries) -> tuple:
+    """Checks that both state-cache calls share; the sizes and types they pass on."""
+    _state_dtype("state", state)
+    if state.dim() != 4 or cache.dim() != 4:
+        raise ValueError("state and cache must be [states, hv, dv, dk]")
+    if cache.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise TypeError("cache must be int8 or float8_e4m3fn")
+    hv, dv, dk = state.shape[1:]
+    _expect("cache", cache, (cache.shape[0], hv, dv, dk))
+    _expect("scales", scales, (cache.shape[0], hv, dv), torch.float32)
+    n = next((t.numel() for t in (slots, entries) if t is not None), min(state.shape[0], cache.shape[0]))
+    _indices("slots", slots, n)
+    _indices("entries", entries, n)
+    _on_device(state.device, state=state, cache=cache, scales=scales, slots=slots, entries=entries)
+    return n, hv, dk, dv, GDN_I8 if cache.dtype == torch.int8 else GDN_E4M3
+
+
+def state_cache_write(state: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, *,
+                      slots: Optional[torch.Tensor] = None, entries: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Quantise states into cache entries (``gdn_state_cache_write``): state
+    [slots, hv, dv, dk] (fp32 or bf16) at ``slots[i]`` goes to cache [entries,
+    hv, dv, dk] (int8 or float8_e4m3fn) and scales [entries, hv, dv] (fp32) at
+    ``entries[i]``, one scale per row of dk values. slots, entries int32 [n] on
+    the device; None counts 0, 1, ... (n from the other one, or with both
+    None as many as both pools hold)."""
+    n, hv, dk, dv, code = _state_cache(state, cache, scales, slots, entries)
+    with _on_stream(state.device, stream) as st:
+        _check(load().gdn_state_cache_write(
+            _ptr(state), _dtype_code(state.dtype), _ptr(slots), state.shape[0], _ptr(cache), code, _ptr(scales),
+            _ptr(entries), cache.shape[0], n, hv, dk, dv, st.cuda_stream or None))
+
+
+def state_cache_read(cache: torch.Tensor, scales: torch.Tensor, state: torch.Tensor, *,
+                     entries: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Put cache entries back into slots of a state pool
+    (``gdn_state_cache_read``): ``state[slots[i]] = cache[entries[i]] *
+    scales[entries[i]]``; arguments as ``state_cache_write``. One entry may go
+    to many slots."""
+    n, hv, dk, dv, code = _state_cache(state, cache, scales, slots, entries)
+    with _on_stream(state.device, stream) as st:
+        _check(load().gdn_state_cache_read(
+            _ptr(cache), code, _ptr(scales), _ptr(entries), cache.shape[0], _ptr(state), _dtype_code(state.dtype),
+            _ptr(slots), state.shape[0], n, hv, dk, dv, st.cuda_stream or None))
 
 
 # gdn_tune_prefill's candidates in its order: (chunk, state rows per scan

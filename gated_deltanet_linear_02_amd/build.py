@@ -21,7 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 ARCH = "gfx950"
 
-SOURCES = ["gdn_api.hip", "gdn_decode.hip", "gdn_norm.hip", "gdn_prefill.hip", "gdn_tune.hip"]
+SOURCES = ["gdn_api.hip", "gdn_decode.hip", "gdn_linattn.hip", "gdn_linattn_api.hip", "gdn_norm.hip",
+           "gdn_prefill.hip", "gdn_state_cache.hip", "gdn_tune.hip"]
 # gdn_prefill_inst.hip is compiled once per (bf16 I/O, chunk size): the
 # chunked prefill's kernels, six objects built in parallel.
 INSTANCES = [("gdn_prefill_inst.hip", f"gdn_prefill_inst_b{b}_c{c}", [f"-DGDN_INST_BF16={b}", f"-DGDN_INST_CHUNK={c}"])

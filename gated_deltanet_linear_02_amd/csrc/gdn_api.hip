@@ -4,6 +4,7 @@
 // carving, dispatch to the kernel launchers, and optional per-kernel event
 // timing. Nothing here allocates device memory.
 #include "gdn.h"
+#include "gdn_checks.hpp"
 #include "gdn_launch.hpp"
 
 #include <algorithm>
@@ -70,27 +71,7 @@ int32_t stream_device_cus(hipStream_t stream) {
 
 // ----------------------------------------------------------------- checks
 
-static bool valid_head(int32_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 static bool valid_chunk(int32_t c) { return c == 0 || c == 1 || c == 16 || c == 32 || c == 64; }
-
-static bool valid_dtype(int32_t t) { return t == GDN_BF16 || t == GDN_F32; }
-static size_t dtype_bytes(int32_t t) { return t == GDN_BF16 ? 2 : 4; }
-
-struct Range {
-    uintptr_t lo, hi;
-};
-static Range span(const void *p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + bytes};
-}
-// Tensors the kernels read or write in 16-byte pieces must start on a
-// 16-byte boundary (their rows are then aligned too: d >= 16).
-static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-static bool overlaps(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
 
 }  // namespace gdn
 

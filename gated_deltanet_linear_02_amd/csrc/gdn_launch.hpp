@@ -13,7 +13,8 @@ namespace gdn {
 
 enum KernelKind {
     kSchedule = 0, kPrep = 1, kScan = 2, kDecode = 3, kTokenScan = 4, kDecodeNorm = 5, kNormApply = 6,
-    kKinds = 7
+    kLinState = 7, kLinJoin = 8, kLinOut = 9, kLinDecode = 10, kCacheWrite = 11, kCacheRead = 12,
+    kKinds = 13
 };
 
 // Per-kernel timing (see gdn_timing_start in gdn.h): while it is active,

@@ -1,0 +1,250 @@
+// gdn_linattn.hip -- linear attention with a decay per head (gfx950): the
+// decode step and the token-by-token prefill.
+//
+// Per (sequence, value head), with a = exp(g):
+//     S <- a S + v k^T,   o = scale S q
+// The delta rule without its correction: nothing of the old state is
+// subtracted along k, so every row of S is scaled and added to, and the
+// output of the new state is scale (a (S q) + v (k.q)) over the old one.
+#include "gdn_linattn.hpp"
+#include "gdn_rows.hpp"
+
+namespace gdn {
+
+// ---------------------------------------------------------------------------
+// Decode: one token per sequence
+// ---------------------------------------------------------------------------
+//
+// Bound by the bytes of the states, read once and written once (64 sequences
+// at 32 heads, d = 128, fp32: 268 MB). Rows of a state are independent: a row
+// is spread over LPR = DK / 8 lanes (StateLane), every lane group takes
+// NRL rows of its workgroup, and q.S, k.q are summed over the lanes of a row
+// by DPP moves. Loads and stores of fp32 states are nontemporal (nothing reads
+// them again before the next step).
+template <typename SE> constexpr int kLinDecodeThreads = 256;
+template <> constexpr int kLinDecodeThreads<bf16> = 1024;
+template <typename SE> constexpr int kLinDecodeRowsPerLane = 1;
+template <> constexpr int kLinDecodeRowsPerLane<bf16> = 2;
+
+template <typename SE, int DK, int DV> struct LinDecodeShape {
+    static constexpr int LPR = DK / 8;  // lanes per state row
+    static constexpr int TMAX = DV * LPR / kLinDecodeRowsPerLane<SE>;
+    static constexpr int THREADS = kLinDecodeThreads<SE> < TMAX ? kLinDecodeThreads<SE> : (TMAX < 64 ? 64 : TMAX);
+    static constexpr int RPP = THREADS / LPR;  // rows per pass of the workgroup
+    static constexpr int NRL =
+        RPP >= DV ? 1 : (kLinDecodeRowsPerLane<SE> < DV / RPP ? kLinDecodeRowsPerLane<SE> : DV / RPP);
+    static constexpr int ROWS = RPP * NRL;  // rows per workgroup
+    static constexpr int SLICES = (DV + ROWS - 1) / ROWS;
+};
+
+template <typename E, typename G, typename SE, int DK, int DV, bool kSlots>
+__global__ __launch_bounds__((LinDecodeShape<SE, DK, DV>::THREADS)) void gdn_linattn_decode_kernel(
+    const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v, const G *__restrict__ gate_g,
+    int32_t gate_ld,  // elements of g from one sequence to the next: hv, or 0 (one gate per head)
+    const SE *state, SE *state_out,  // may be the same pool
+    const int32_t *__restrict__ slots, int32_t num_slots, E *__restrict__ out, int32_t hk, int32_t hv, float scale)
+{
+    typedef LinDecodeShape<SE, DK, DV> SH;
+    typedef StateLane<SE, SH::LPR> SL;
+    constexpr int LPR = SH::LPR, RPP = SH::RPP, NRL = SH::NRL, ROWS = SH::ROWS, SLICES = SH::SLICES;
+
+    const int bhs = blockIdx.x;
+    const int bh = bhs / SLICES;
+    const int row0 = (bhs - bh * SLICES) * ROWS;
+    const int b = bh / hv;
+    const int h = bh - b * hv;
+    const int kh = h / (hv / hk);
+    const int tid = threadIdx.x;
+    const int lr = tid % LPR;
+    const int r0 = row0 + tid / LPR;  // this lane group's rows: r0 + p RPP, p < NRL
+
+    const int slot = kSlots ? slots[b] : b;
+    E *o_row = out + ((size_t)b * hv + h) * DV;
+    if (kSlots && (slot < 0 || slot >= num_slots)) {
+#pragma unroll
+        for (int p = 0; p < NRL; ++p)
+            if (r0 + p * RPP < DV && lr == 0) o_row[r0 + p * RPP] = from_f32<E>(0.0f);
+        return;
+    }
+    const size_t base = ((size_t)slot * hv + h) * (size_t)(DV * DK);
+
+    float s[NRL][8];
+#pragma unroll
+    for (int p = 0; p < NRL; ++p) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[p][j] = 0.f;
+        if (r0 + p * RPP < DV) SL::load(state + base + (size_t)(r0 + p * RPP) * DK, lr, s[p]);
+    }
+    float kk[8], qq[8];
+    const size_t kq0 = ((size_t)b * hk + kh) * DK;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        load4<E>(k + kq0 + SL::col(lr, 4 * m), kk + 4 * m);
+        load4<E>(q + kq0 + SL::col(lr, 4 * m), qq + 4 * m);
+    }
+    const float a = expf(static_cast<float>(gate_g[(size_t)b * gate_ld + h]));
+    float vv[NRL];
+#pragma unroll
+    for (int p = 0; p < NRL; ++p)
+        vv[p] = r0 + p * RPP < DV ? static_cast<float>(v[((size_t)b * hv + h) * DV + r0 + p * RPP]) : 0.f;
+
+    float kq = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) kq = __builtin_fmaf(kk[j], qq[j], kq);
+    kq = row_sum<LPR>(kq);
+#pragma unroll
+    for (int p = 0; p < NRL; ++p) {
+        float sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(s[p][j], qq[j], sq);
+        sq = row_sum<LPR>(sq);
+        const int row = r0 + p * RPP;
+        if (row < DV) {
+            if (lr == 0) o_row[row] = from_f32<E>(scale * __builtin_fmaf(a, sq, kq * vv[p]));
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __builtin_fmaf(a, s[p][j], vv[p] * kk[j]);
+            SL::store(state_out + base + (size_t)row * DK, lr, w);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Prefill, token by token
+// ---------------------------------------------------------------------------
+//
+// A workgroup holds 256 / LPR rows of one (sequence, value head) state and
+// applies every token of the sequence in order.
+template <typename E, typename G, typename SE, int DK, int DV>
+__global__ __launch_bounds__(256) void gdn_linattn_token_kernel(
+    const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v, const G *__restrict__ gate_g,
+    int32_t gate_ld, const int32_t *__restrict__ cu, int32_t total_tokens, const SE *s0, SE *sfin,
+    E *__restrict__ out, int32_t hk, int32_t hv, float scale)
+{
+    constexpr int LPR = DK / 8, ROWS = 256 / LPR, SLICES = (DV + ROWS - 1) / ROWS;
+    typedef StateLane<SE, LPR> SL;
+    const int nhs = blockIdx.x;
+    const int nh = nhs / SLICES;
+    const int n = nh / hv, h = nh - n * hv, kh = h / (hv / hk);
+    const int tid = threadIdx.x, lane = tid & 63, lr = tid % LPR;
+    const int row = (nhs - nh * SLICES) * ROWS + tid / LPR;
+
+    // Offsets clamped into [0, T] and made non-decreasing.
+    auto clampT = [&](int x) { return min(max(x, 0), total_tokens); };
+    int lo = clampT(cu[0]), hi = lo;
+    for (int j = lane; j <= n; j += 64) {
+        const int e = clampT(cu[j + 1]);
+        hi = max(hi, e);
+        if (j < n) lo = max(lo, e);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        hi = max(hi, __shfl_xor(hi, off));
+        lo = max(lo, __shfl_xor(lo, off));
+    }
+    const size_t base = ((size_t)n * hv + h) * (size_t)(DV * DK) + (size_t)row * DK;
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    if (s0 && row < DV) SL::load(s0 + base, lr, s);
+    for (int t = lo; t < hi; ++t) {
+        float kk[8], qq[8];
+        const size_t kq0 = ((size_t)t * hk + kh) * DK;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            load4<E>(k + kq0 + SL::col(lr, 4 * m), kk + 4 * m);
+            load4<E>(q + kq0 + SL::col(lr, 4 * m), qq + 4 * m);
+        }
+        const float a = expf(static_cast<float>(gate_g[(size_t)t * gate_ld + h]));
+        const float vv = row < DV ? static_cast<float>(v[((size_t)t * hv + h) * DV + row]) : 0.f;
+        float o = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            s[j] = __builtin_fmaf(a, s[j], vv * kk[j]);
+            o = __builtin_fmaf(s[j], qq[j], o);
+        }
+        o = row_sum<LPR>(o);
+        if (row < DV && lr == 0) out[((size_t)t * hv + h) * DV + row] = from_f32<E>(scale * o);
+    }
+    if (sfin && row < DV) SL::store(sfin + base, lr, s);
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+
+// Calls f(DK, DV) as integral constants for the built head sizes.
+template <typename F> static hipError_t with_heads(int dk, int dv, F f) {
+    auto inner = [&](auto kc) {
+        switch (dv) {
+        case 16: return f(kc, std::integral_constant<int, 16>());
+        case 32: return f(kc, std::integral_constant<int, 32>());
+        case 64: return f(kc, std::integral_constant<int, 64>());
+        case 128: return f(kc, std::integral_constant<int, 128>());
+        default: return hipErrorInvalidValue;
+        }
+    };
+    switch (dk) {
+    case 16: return inner(std::integral_constant<int, 16>());
+    case 32: return inner(std::integral_constant<int, 32>());
+    case 64: return inner(std::integral_constant<int, 64>());
+    case 128: return inner(std::integral_constant<int, 128>());
+    default: return hipErrorInvalidValue;
+    }
+}
+
+// Calls f(E, G, SE) as values of the built element, gate and state types
+// (bf16 states with bf16 I/O only).
+template <typename F> static hipError_t with_types(bool io_bf16, bool gate_bf16, bool state_bf16, F f) {
+    if (io_bf16) {
+        if (state_bf16) return gate_bf16 ? f(bf16(), bf16(), bf16()) : f(bf16(), float(), bf16());
+        return gate_bf16 ? f(bf16(), bf16(), float()) : f(bf16(), float(), float());
+    }
+    if (state_bf16) return hipErrorInvalidValue;
+    return gate_bf16 ? f(float(), bf16(), float()) : f(float(), float(), float());
+}
+
+int32_t linattn_decode_slices(int32_t dk, int32_t dv, bool state_bf16) {
+    int32_t n = 0;
+    (void)with_heads(dk, dv, [&](auto kc, auto vc) {
+        n = state_bf16 ? LinDecodeShape<bf16, kc(), vc()>::SLICES : LinDecodeShape<float, kc(), vc()>::SLICES;
+        return hipSuccess;
+    });
+    return n;
+}
+
+hipError_t launch_linattn_decode(const LinDecodeArgs &A, hipStream_t st) {
+    return with_types(A.io_bf16, A.gate_bf16, A.state_bf16, [&](auto e, auto g, auto se) {
+        typedef decltype(e) E;
+        typedef decltype(g) G;
+        typedef decltype(se) SE;
+        return with_heads(A.dk, A.dv, [&](auto kc, auto vc) {
+            constexpr int DK = kc(), DV = vc();
+            typedef LinDecodeShape<SE, DK, DV> SH;
+            const dim3 grid((unsigned)A.batch * (unsigned)A.hv * (unsigned)SH::SLICES), block(SH::THREADS);
+            const auto kernel = A.slots ? gdn_linattn_decode_kernel<E, G, SE, DK, DV, true>
+                                        : gdn_linattn_decode_kernel<E, G, SE, DK, DV, false>;
+            return launch_kernel(kLinDecode, kernel, grid, block, 0, st, (const E *)A.q, (const E *)A.k,
+                                 (const E *)A.v, (const G *)A.g, A.gate_per_head ? 0 : A.hv, (const SE *)A.state,
+                                 (SE *)A.state_out, A.slots, A.num_slots, (E *)A.out, A.hk, A.hv, A.scale);
+        });
+    });
+}
+
+hipError_t launch_linattn_prefill(const LinPrefillArgs &A, hipStream_t st) {
+    return with_types(A.io_bf16, A.gate_bf16, A.state_bf16, [&](auto e, auto g, auto se) {
+        typedef decltype(e) E;
+        typedef decltype(g) G;
+        typedef decltype(se) SE;
+        return with_heads(A.dk, A.dv, [&](auto kc, auto vc) {
+            constexpr int DK = kc(), DV = vc(), ROWS = 256 / (DK / 8);
+            const dim3 grid((unsigned)A.num_seqs * (unsigned)A.hv * (unsigned)((DV + ROWS - 1) / ROWS)), block(256);
+            return launch_kernel(kLinOut, gdn_linattn_token_kernel<E, G, SE, DK, DV>, grid, block, 0, st,
+                                 (const E *)A.q, (const E *)A.k, (const E *)A.v, (const G *)A.g,
+                                 A.gate_per_head ? 0 : A.hv, A.cu, (int32_t)A.total_tokens, (const SE *)A.s0,
+                                 (SE *)A.s_final, (E *)A.out, A.hk, A.hv, A.scale);
+        });
+    });
+}
+
+}  // namespace gdn

@@ -1,0 +1,56 @@
+// gdn_linattn.hpp -- internal host-side interface of the linear attention
+// with decay (gdn_linattn_api.hip to the kernel launchers). Not part of the
+// ABI.
+#pragma once
+
+#include "gdn_launch.hpp"
+
+namespace gdn {
+
+struct LinPrefillArgs {
+    const void *q, *k, *v, *g;
+    const int32_t *cu;
+    int32_t num_seqs;
+    int64_t total_tokens;
+    int32_t hk, hv, dk, dv;
+    float scale;
+    bool io_bf16, gate_bf16, state_bf16;
+    bool gate_per_head;  // g is [hv], not [T][hv]
+    const void *s0;
+    void *s_final;
+    void *out;
+    char *ws;
+};
+hipError_t launch_linattn_prefill(const LinPrefillArgs &a, hipStream_t st);
+
+struct LinDecodeArgs {
+    const void *q, *k, *v, *g;
+    const void *state;
+    void *state_out;  // may be `state`
+    const int32_t *slots;
+    int32_t num_slots;
+    void *out;
+    int32_t batch, hk, hv, dk, dv;
+    float scale;
+    bool io_bf16, gate_bf16, state_bf16, gate_per_head;
+};
+hipError_t launch_linattn_decode(const LinDecodeArgs &a, hipStream_t st);
+
+// Workgroups per (sequence, value head) that launch_linattn_decode takes.
+int32_t linattn_decode_slices(int32_t dk, int32_t dv, bool state_bf16);
+
+struct StateCacheArgs {
+    void *state;            // written by a read, read by a write
+    const int32_t *slots;   // NULL: the identity
+    int32_t num_slots;
+    void *cache;
+    float *scales;
+    const int32_t *entries;
+    int32_t num_entries;
+    int32_t n, hv, dk, dv;
+    bool state_bf16, e4m3;
+};
+hipError_t launch_state_cache_write(const StateCacheArgs &a, hipStream_t st);
+hipError_t launch_state_cache_read(const StateCacheArgs &a, hipStream_t st);
+
+}  // namespace gdn

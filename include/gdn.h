@@ -402,6 +402,106 @@ int32_t gdn_tune_cache_save(const char *path);
 int32_t gdn_tune_cache_load(const char *path, int32_t *entries);
 
 /*
+ * Linear attention with a decay for each head
+ * -------------------------------------------
+ * The recurrence of the layer above without the delta rule's correction, as
+ * models mix it with Gated DeltaNet layers:
+ *
+ *     a_t = exp(g_t)
+ *     S_t = a_t S_{t-1} + v_t k_t^T
+ *     o_t = scale * S_t q_t
+ *
+ * Layouts, types, streams and errors are those of gdn_prefill and
+ * gdn_decode_step, with these differences:
+ * - dk and dv need not be equal: 16, 32, 64 or 128 each.
+ * - gate_per_head 0: g is [T][hv] (decode: [B][hv]), one gate per token and
+ *   head; 1: g is [hv], one per head for every token. g may be -infinity (the
+ *   state is forgotten); it must not be NaN or +infinity.
+ * - state_dtype GDN_F32 or GDN_BF16 is the element type of the states;
+ *   GDN_BF16 needs io_dtype GDN_BF16. The arithmetic on states is fp32 with
+ *   either (a prefill rounds the final state once, a decode step the new one).
+ * - k, q, v must be finite: what follows a non-finite value in its sequence
+ *   is not defined, nor are the up to 63 tokens before it. Other sequences are
+ *   untouched by it.
+ *
+ * gdn_linattn_prefill: every token of N packed sequences. cu_seqlens as for
+ * gdn_prefill (DEVICE, clamped into [0, total_tokens] and made non-decreasing);
+ * tokens outside [cu_seqlens[0], cu_seqlens[N]) are neither read nor written;
+ * the final state of an empty sequence is its initial state.
+ * max_seqlen   the longest sequence's length if the host knows it, else 0; it
+ *              steers how the work is split, never what is computed. Errors
+ *              as for gdn_prefill_hint.
+ * initial_state, final_state  [N][hv][dv][dk] in state_dtype, or NULL (zeros;
+ *              not written). They may be the same buffer.
+ * workspace    at least gdn_linattn_prefill_workspace_size(...) bytes for the
+ *              same sizes and max_seqlen, 256-byte aligned, not shared by calls
+ *              that may overlap. Where that size is 256 it is not touched and
+ *              may be NULL.
+ *
+ * gdn_linattn_decode_step: one token for each of `batch` sequences.
+ * state_out    NULL or `state`: the states are updated in place. Otherwise a
+ *              second pool of the same sizes that shares no byte with `state`:
+ *              the new states go to the same slots there and `state` stays as
+ *              it was, so that a drafted token can be taken back.
+ * state_slots, num_slots  as for gdn_decode_step (a slot outside
+ *              [0, num_slots): the sequence is skipped, its output zeros; two
+ *              sequences of one call must not share a slot).
+ */
+size_t gdn_linattn_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
+                                          int32_t hk, int32_t hv, int32_t dk, int32_t dv, int32_t io_dtype);
+int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const void *g,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
+                            int32_t hk, int32_t hv, int32_t dk, int32_t dv, float scale,
+                            int32_t io_dtype, int32_t gate_dtype, int32_t gate_per_head,
+                            const void *initial_state, void *final_state, int32_t state_dtype, void *out,
+                            void *workspace, size_t workspace_bytes, void *stream);
+int32_t gdn_linattn_decode_step(const void *q, const void *k, const void *v, const void *g,
+                                int32_t batch, int32_t hk, int32_t hv, int32_t dk, int32_t dv, float scale,
+                                int32_t io_dtype, int32_t gate_dtype, int32_t gate_per_head,
+                                void *state, void *state_out, int32_t state_dtype,
+                                const int32_t *state_slots, int32_t num_slots, void *out, void *stream);
+
+/*
+ * States in an 8-bit cache
+ * ------------------------
+ * A recurrent layer's cache is its states: a prefix's state taken up by later
+ * requests, a sequence put aside. gdn_state_cache_write quantises states of
+ * a pool as it puts them into cache entries; gdn_state_cache_read puts entries
+ * back into slots of a pool. For the states of either recurrence of this
+ * library. Per row of dk values (fp32 arithmetic, the codes those of the exact
+ * quotient):
+ *
+ *     scale = max|x| / M,   code = x / scale to the nearest (ties to even)
+ *     read back: code * scale, rounded to the state's type
+ *
+ * with M = 127 for GDN_I8 (codes -127 .. 127) and 448 for GDN_E4M3 (e4m3
+ * without infinities, 448 its largest value). A row of zeros has scale 0; a
+ * row with a NaN or an infinity gets scale NaN and reads back as NaN. Where
+ * M * scale would overflow, the scale is the next smaller number. Rows below
+ * 2^-110 lose accuracy as their scale underflows.
+ * Step the state itself in fp32 or bf16 and quantise it when it is put away:
+ * rounding to 8 bits at every token would add up.
+ *
+ * state        [num_slots][hv][dv][dk] in state_dtype.
+ * cache        [num_entries][hv][dv][dk], one byte each.
+ * scales       fp32 [num_entries][hv][dv].
+ * slots, entries  int32 [n] DEVICE arrays, or NULL for 0 .. n - 1: item i
+ *              is slot slots[i] and entry entries[i]. An item whose slot or
+ *              entry lies outside its pool is skipped. What is read may be
+ *              named many times (one prefix for many sequences), what is
+ *              written once per call.
+ * dk, dv       16, 32, 64 or 128 each.
+ */
+typedef enum { GDN_I8 = 0, GDN_E4M3 = 1 } gdn_cache_dtype;
+
+int32_t gdn_state_cache_write(const void *state, int32_t state_dtype, const int32_t *slots, int32_t num_slots,
+                              void *cache, int32_t cache_dtype, float *scales, const int32_t *entries,
+                              int32_t num_entries, int32_t n, int32_t hv, int32_t dk, int32_t dv, void *stream);
+int32_t gdn_state_cache_read(const void *cache, int32_t cache_dtype, const float *scales, const int32_t *entries,
+                             int32_t num_entries, void *state, int32_t state_dtype, const int32_t *slots,
+                             int32_t num_slots, int32_t n, int32_t hv, int32_t dk, int32_t dv, void *stream);
+
+/*
  * Per-kernel timing (a profiling aid, not needed for computation).
  *
  * gdn_timing_start(max_launches) makes the library time each of its next
@@ -414,10 +514,12 @@ int32_t gdn_tune_cache_load(const char *path, int32_t *entries);
  * releases the events and stops timing. Kinds: 0 = varlen schedule,
  * 1 = chunk preparation, 2 = chunk-recurrent scan, 3 = decode step,
  * 4 = token-by-token prefill, 5 = decode step with output normalisation,
- * 6 = output normalisation pass of the prefill.
+ * 6 = output normalisation pass of the prefill, 7, 8, 9 = segment states,
+ * their joining, and outputs of the linear attention prefill, 10 = linear
+ * attention decode step, 11 = state cache write, 12 = state cache read.
  * Not thread-safe with concurrent gdn_* calls from other host threads.
  */
-#define GDN_KERNEL_KINDS 7
+#define GDN_KERNEL_KINDS 13
 int32_t gdn_timing_start(int32_t max_launches);
 int32_t gdn_timing_stop(int32_t *counts, float *total_ms, int32_t n_kinds);
 
