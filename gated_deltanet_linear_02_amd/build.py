@@ -27,6 +27,9 @@ SOURCES = ["gdn_api.hip", "gdn_decode.hip", "gdn_linattn.hip", "gdn_linattn_api.
 # chunked prefill's kernels, six objects built in parallel.
 INSTANCES = [("gdn_prefill_inst.hip", f"gdn_prefill_inst_b{b}_c{c}", [f"-DGDN_INST_BF16={b}", f"-DGDN_INST_CHUNK={c}"])
              for b in (1, 0) for c in (64, 32, 16)]
+# gdn_linattn_inst.hip likewise, once per (bf16 I/O, dk).
+INSTANCES += [("gdn_linattn_inst.hip", f"gdn_linattn_inst_b{b}_k{d}", [f"-DGDN_INST_BF16={b}", f"-DGDN_INST_DK={d}"])
+              for b in (1, 0) for d in (128, 64, 32, 16)]
 
 # Packed-fp32 VALU forms are disabled; hipcc's host pass warns that it does
 # not know the feature, which is harmless.

@@ -1,5 +1,5 @@
 // gdn_linattn.hip -- linear attention with a decay per head (gfx950): the
-// decode step and the token-by-token prefill.
+// decode step, and how a prefill is split and dispatched.
 //
 // Per (sequence, value head), with a = exp(g):
 //     S <- a S + v k^T,   o = scale S q
@@ -110,66 +110,6 @@ __global__ __launch_bounds__((LinDecodeShape<SE, DK, DV>::THREADS)) void gdn_lin
 }
 
 // ---------------------------------------------------------------------------
-// Prefill, token by token
-// ---------------------------------------------------------------------------
-//
-// A workgroup holds 256 / LPR rows of one (sequence, value head) state and
-// applies every token of the sequence in order.
-template <typename E, typename G, typename SE, int DK, int DV>
-__global__ __launch_bounds__(256) void gdn_linattn_token_kernel(
-    const E *__restrict__ q, const E *__restrict__ k, const E *__restrict__ v, const G *__restrict__ gate_g,
-    int32_t gate_ld, const int32_t *__restrict__ cu, int32_t total_tokens, const SE *s0, SE *sfin,
-    E *__restrict__ out, int32_t hk, int32_t hv, float scale)
-{
-    constexpr int LPR = DK / 8, ROWS = 256 / LPR, SLICES = (DV + ROWS - 1) / ROWS;
-    typedef StateLane<SE, LPR> SL;
-    const int nhs = blockIdx.x;
-    const int nh = nhs / SLICES;
-    const int n = nh / hv, h = nh - n * hv, kh = h / (hv / hk);
-    const int tid = threadIdx.x, lane = tid & 63, lr = tid % LPR;
-    const int row = (nhs - nh * SLICES) * ROWS + tid / LPR;
-
-    // Offsets clamped into [0, T] and made non-decreasing.
-    auto clampT = [&](int x) { return min(max(x, 0), total_tokens); };
-    int lo = clampT(cu[0]), hi = lo;
-    for (int j = lane; j <= n; j += 64) {
-        const int e = clampT(cu[j + 1]);
-        hi = max(hi, e);
-        if (j < n) lo = max(lo, e);
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        hi = max(hi, __shfl_xor(hi, off));
-        lo = max(lo, __shfl_xor(lo, off));
-    }
-    const size_t base = ((size_t)n * hv + h) * (size_t)(DV * DK) + (size_t)row * DK;
-    float s[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = 0.f;
-    if (s0 && row < DV) SL::load(s0 + base, lr, s);
-    for (int t = lo; t < hi; ++t) {
-        float kk[8], qq[8];
-        const size_t kq0 = ((size_t)t * hk + kh) * DK;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            load4<E>(k + kq0 + SL::col(lr, 4 * m), kk + 4 * m);
-            load4<E>(q + kq0 + SL::col(lr, 4 * m), qq + 4 * m);
-        }
-        const float a = expf(static_cast<float>(gate_g[(size_t)t * gate_ld + h]));
-        const float vv = row < DV ? static_cast<float>(v[((size_t)t * hv + h) * DV + row]) : 0.f;
-        float o = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s[j] = __builtin_fmaf(a, s[j], vv * kk[j]);
-            o = __builtin_fmaf(s[j], qq[j], o);
-        }
-        o = row_sum<LPR>(o);
-        if (row < DV && lr == 0) out[((size_t)t * hv + h) * DV + row] = from_f32<E>(scale * o);
-    }
-    if (sfin && row < DV) SL::store(sfin + base, lr, s);
-}
-
-// ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 
@@ -231,20 +171,39 @@ hipError_t launch_linattn_decode(const LinDecodeArgs &A, hipStream_t st) {
     });
 }
 
+// ---------------------------------------------------------------------------
+// Prefill
+// ---------------------------------------------------------------------------
+
+// Sequences are cut where whole ones would leave compute units idle.
+LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv) {
+    constexpr int64_t kWorkgroups = 512, kLeast = 256;
+    LinPlan P;
+    P.items = num_seqs;
+    const int64_t longest = max_seqlen ? max_seqlen : total_tokens;
+    int shift = 6;
+    while ((int64_t)1 << shift < kLeast || ((int64_t)kWorkgroups << shift) < total_tokens * hv) ++shift;
+    if (longest <= (int64_t)1 << shift) return P;
+    P.seg_shift = shift;
+    P.items = (total_tokens >> shift) + num_seqs;
+    P.off_state = 0;
+    P.off_decay = align256((size_t)P.items * hv * dk * dv * sizeof(float));
+    P.total = align256(P.off_decay + (size_t)P.items * hv * sizeof(float));
+    return P;
+}
+
 hipError_t launch_linattn_prefill(const LinPrefillArgs &A, hipStream_t st) {
-    return with_types(A.io_bf16, A.gate_bf16, A.state_bf16, [&](auto e, auto g, auto se) {
-        typedef decltype(e) E;
-        typedef decltype(g) G;
-        typedef decltype(se) SE;
-        return with_heads(A.dk, A.dv, [&](auto kc, auto vc) {
-            constexpr int DK = kc(), DV = vc(), ROWS = 256 / (DK / 8);
-            const dim3 grid((unsigned)A.num_seqs * (unsigned)A.hv * (unsigned)((DV + ROWS - 1) / ROWS)), block(256);
-            return launch_kernel(kLinOut, gdn_linattn_token_kernel<E, G, SE, DK, DV>, grid, block, 0, st,
-                                 (const E *)A.q, (const E *)A.k, (const E *)A.v, (const G *)A.g,
-                                 A.gate_per_head ? 0 : A.hv, A.cu, (int32_t)A.total_tokens, (const SE *)A.s0,
-                                 (SE *)A.s_final, (E *)A.out, A.hk, A.hv, A.scale);
-        });
-    });
+    switch (A.dk + A.io_bf16) {
+    case 16: return launch_linattn_chunk_k<0, 16>(A, st);
+    case 17: return launch_linattn_chunk_k<1, 16>(A, st);
+    case 32: return launch_linattn_chunk_k<0, 32>(A, st);
+    case 33: return launch_linattn_chunk_k<1, 32>(A, st);
+    case 64: return launch_linattn_chunk_k<0, 64>(A, st);
+    case 65: return launch_linattn_chunk_k<1, 64>(A, st);
+    case 128: return launch_linattn_chunk_k<0, 128>(A, st);
+    case 129: return launch_linattn_chunk_k<1, 128>(A, st);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace gdn

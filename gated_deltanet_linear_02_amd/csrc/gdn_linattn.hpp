@@ -7,6 +7,17 @@
 
 namespace gdn {
 
+// How a prefill is split: whole sequences (seg_shift < 0), or segments of
+// 2^seg_shift tokens whose states go through the workspace.
+struct LinPlan {
+    int32_t seg_shift = -1;
+    int64_t items = 0;          // sequences, or the bound on segments
+    size_t off_state = 0;       // float [items][hv][dv * dk], accumulator order
+    size_t off_decay = 0;       // float [items][hv]
+    size_t total = 0;           // bytes of workspace
+};
+LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv);
+
 struct LinPrefillArgs {
     const void *q, *k, *v, *g;
     const int32_t *cu;
@@ -20,7 +31,10 @@ struct LinPrefillArgs {
     void *s_final;
     void *out;
     char *ws;
+    LinPlan plan;
 };
+// Chunk by chunk, one instantiation per I/O type and dk (gdn_linattn_inst.hip).
+template <int kIoBf16, int DK> hipError_t launch_linattn_chunk_k(const LinPrefillArgs &a, hipStream_t st);
 hipError_t launch_linattn_prefill(const LinPrefillArgs &a, hipStream_t st);
 
 struct LinDecodeArgs {

@@ -5,6 +5,8 @@
 #include "gdn_checks.hpp"
 #include "gdn_linattn.hpp"
 
+#include <algorithm>
+
 using namespace gdn;
 
 // Sizes and types that both linear-attention calls share.
@@ -27,8 +29,10 @@ static int32_t check_linattn_prefill(int32_t num_seqs, int64_t total_tokens, int
     if (max_seqlen != 0 &&
         (max_seqlen < 0 || max_seqlen > total_tokens || max_seqlen * (int64_t)num_seqs < total_tokens))
         return GDN_ERR_BAD_VALUE;
-    // One workgroup per (sequence, value head, row slice) at least.
-    if ((int64_t)num_seqs * hv * dv > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    // The grids: items (segments, or sequences) x heads, 64 workgroups of the
+    // join per (sequence, head) at most.
+    const int64_t items = total_tokens / 64 + num_seqs + 8;
+    if ((double)items * hv > INT32_MAX || (double)num_seqs * hv * 64 > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -39,7 +43,7 @@ size_t gdn_linattn_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens
     if (check_linattn_prefill(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv, io_dtype, GDN_F32, 0, GDN_F32) !=
         GDN_OK)
         return 0;
-    return 256;
+    return std::max<size_t>(256, linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv).total);
 }
 
 int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const void *g, const int32_t *cu_seqlens,
@@ -55,10 +59,9 @@ int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const v
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(initial_state) ||
         !aligned16(final_state))
         return GDN_ERR_MISALIGNED;
-    const size_t need = gdn_linattn_prefill_workspace_size(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv,
-                                                           io_dtype);
-    const size_t used = need > 256 ? need : 0;
-    if (used && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    const LinPlan plan = linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv);
+    const size_t used = plan.total;
+    if (used && (!workspace || workspace_bytes < used || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return GDN_ERR_WORKSPACE;
 
     const size_t T = (size_t)total_tokens, eb = dtype_bytes(io_dtype), gb = dtype_bytes(gate_dtype);
@@ -81,6 +84,7 @@ int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const v
     A.io_bf16 = io_dtype == GDN_BF16; A.gate_bf16 = gate_dtype == GDN_BF16; A.state_bf16 = state_dtype == GDN_BF16;
     A.gate_per_head = gate_per_head != 0;
     A.s0 = initial_state; A.s_final = final_state; A.out = out; A.ws = static_cast<char *>(workspace);
+    A.plan = plan;
     try {
         return launch_linattn_prefill(A, static_cast<hipStream_t>(stream)) == hipSuccess ? GDN_OK : GDN_ERR_HIP;
     } catch (...) {

@@ -1,0 +1,679 @@
+// gdn_linattn_chunk.hpp -- linear attention with a decay per head, chunk by
+// chunk (gfx950).
+//
+// A chunk of C tokens starts from the state S0 (dv x dk). With c_t the sum of
+// the gates from the chunk's first token to t, gamma_t = exp(c_t) and
+// delta_t = exp(c_C - c_t):
+//     o_i = scale ( gamma_i S0 q_i + sum_{j <= i} exp(c_i - c_j) (q_i . k_j) v_j )
+//     S  <- gamma_C S0 + sum_t (delta_t v_t) k_t^T
+// All sums are matrix products. Sums of gates are kept in fp64 (in units of
+// log 2) and every factor is formed from a difference of them, so that a decay
+// to nothing inside the chunk costs its neighbours no accuracy.
+//
+// A workgroup owns one (sequence or segment, value head) state for its whole
+// run: the fp32 state stays in the accumulators of its waves, S^T in 16 x 16
+// tiles (rows over dk), each wave holding all dk of 16 dv columns. An
+// accumulator tile is an operand of the next product as it stands, so the state
+// never leaves the registers:
+//     O^T[dv][i]  = S0 Q^T          state tiles (bf16) x Q rows from LDS
+//                 + V^T P^T         V columns x the scores P from LDS
+//     S^T[dk][dv] += K^T (delta V)  K columns from LDS x V columns
+// Columns (operands that run over tokens) are read from row-major LDS with the
+// transposing LDS read.
+//
+// With bf16 I/O the products are bf16 MFMAs with fp32 sums. Rounded on the way
+// are the operand copy of S0 and the scores P, each once to bf16, as the output
+// itself is. The state is fp32 and must not lose what it sums over
+// thousands of tokens: delta_t v_t is split in three bf16 parts that hold all
+// its 24 bits, and their products with k_t (bf16 already) are exact.
+#pragma once
+
+#include <type_traits>
+
+#include "gdn_device.hpp"
+#include "gdn_linattn.hpp"
+
+#define GDN_SCHED_BARRIER() __builtin_amdgcn_sched_barrier(0)
+
+namespace gdn {
+
+// ------------------------------------------------------------- operands
+
+// A contraction of length K: bf16 MFMAs 32 (or, for K = 16, 16) deep, or fp32,
+// where four 4-deep MFMAs make one 16-deep step. A lane (m = lane % 16, g =
+// lane / 16) holds the KPL contraction indices of acc_k: 4 g .. 4 g + 3 of
+// each 16.
+template <typename E, int K> struct LinOp;
+template <int K> struct LinOp<bf16, K> : Mma<bf16, K> {};
+template <int K> struct LinOp<float, K> {
+    static constexpr int KW = 16, KPL = 4;
+    typedef f32x4 Frag;
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Where index k (a multiple of 4) of a contraction over tokens stands in an LDS
+// row, so that a lane's KPL indices are contiguous.
+template <typename OP> __device__ __forceinline__ constexpr int frag_pos(int k) {
+    if constexpr (OP::KPL == 8) return (k & ~31) | ((k & 12) << 1) | ((k & 16) >> 2);
+    else return k;
+}
+// Contractions over dk take their indices in natural order: lane group g has
+// KPL side by side. So that state tiles are operands of it as they stand,
+// rows 4 g + r of tiles 2 b and 2 b + 1 are (KPL = 8) dk 32 b + 8 g + r and
+// 32 b + 8 g + 4 + r; with KPL = 4 tile t is dk 16 t .. 16 t + 15.
+template <typename OP> __device__ __forceinline__ constexpr int tile_base(int t) {
+    return OP::KPL == 8 ? 32 * (t >> 1) + 4 * (t & 1) : 16 * t;
+}
+// Fragment kb of row (r0 + lane % 16).
+template <typename OP, typename E>
+__device__ __forceinline__ typename OP::Frag row_frag(const E *base, int ld, int r0, int kb, int lane) {
+    return *reinterpret_cast<const typename OP::Frag *>(base + (r0 + (lane & 15)) * ld + kb * OP::KW +
+                                                        OP::KPL * (lane >> 4));
+}
+
+typedef __attribute__((address_space(3))) s16x4 LdsQuad;
+
+// Four tokens of one column. Lane (m, g) gets rows t0 + 4 g .. + 3 of column
+// col(m), where col(m) = c0 + stride (m / 4) + m % 4 and `stride` is the
+// distance of the column groups: 4 (16 columns side by side) or 8.
+// bf16: the transposing read takes, from each 16 lanes, four rows of four
+// 8-byte pieces (lane i: row i / 4, piece i % 4) and hands lane i column i.
+template <typename E>
+__device__ __forceinline__ auto col_quad(const E *base, int ld, int t0, int c0, int stride, int lane) {
+    const int m = lane & 15, g = lane >> 4;
+    if constexpr (std::is_same<E, bf16>::value) {
+        const E *p = base + (t0 + 4 * g + (m >> 2)) * ld + c0 + stride * (m & 3);
+        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsQuad *)p));
+    } else {
+        const E *p = base + (t0 + 4 * g) * ld + c0 + stride * (m >> 2) + (m & 3);
+        return f32x4{p[0], p[ld], p[2 * ld], p[3 * ld]};
+    }
+}
+// Fragment kb of a contraction over tokens, for 16 columns.
+template <typename OP, typename E>
+__device__ __forceinline__ typename OP::Frag col_frag(const E *base, int ld, int kb, int c0, int stride, int lane) {
+    if constexpr (OP::KPL == 8) {
+        const bf16x4 lo = col_quad(base, ld, kb * 32, c0, stride, lane),
+                     hi = col_quad(base, ld, kb * 32 + 16, c0, stride, lane);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+        return col_quad(base, ld, kb * 16, c0, stride, lane);
+    }
+}
+// Fragment kb of a contraction over the rows of accumulator tiles t[16-row tile].
+template <typename OP, typename E> __device__ __forceinline__ typename OP::Frag acc_frag(const f32x4 *t, int kb) {
+    if constexpr (std::is_same<E, float>::value) {
+        return t[kb];
+    } else {
+        typename OP::Frag f;
+#pragma unroll
+        for (int e = 0; e < OP::KPL; ++e) f[e] = static_cast<bf16>(t[kb * (OP::KPL / 4) + e / 4][e & 3]);
+        return f;
+    }
+}
+
+// ------------------------------------------------------------- work split
+
+// The work of one launch. Unsplit (seg_shift < 0): item i is sequence i.
+// Otherwise sequences are cut into segments of L = 2^seg_shift tokens; sequence
+// n's segments are items floor(start_n / L) + n and following (start_n its
+// first token), which leaves room for all of them whatever the lengths,
+// needs no table, and is less than floor(T / L) + N in all.
+struct LinWork {
+    const int32_t *cu;
+    int32_t num_seqs, total_tokens, seg_shift;
+    uint32_t hk, group;  // query/key heads, value heads on each
+    uint32_t units;      // items x hk
+};
+struct LinItem {
+    int seq, seg;  // seg: which segment of the sequence
+    int segs;      // how many it has (an empty sequence has one, empty)
+    int lo, hi;    // the item's tokens
+    bool none;
+};
+
+// Moves across the wave on DPP; lanes that have no source keep x.
+template <int Ctrl, int RowMask> __device__ __forceinline__ int dpp_keep(int x) {
+    return __builtin_amdgcn_update_dpp(x, x, Ctrl, RowMask, 0xf, false);
+}
+// Running maximum over the lanes: within rows of 16, then rows 1 and 3 take
+// row 0's and 2's last, then lanes 32 .. 63 lane 31's.
+__device__ __forceinline__ int wave_scan_max(int x) {
+    x = max(x, dpp_keep<0x111, 0xf>(x));  // row_shr 1
+    x = max(x, dpp_keep<0x112, 0xf>(x));
+    x = max(x, dpp_keep<0x114, 0xf>(x));
+    x = max(x, dpp_keep<0x118, 0xf>(x));
+    x = max(x, dpp_keep<0x142, 0xa>(x));  // row_bcast 15
+    x = max(x, dpp_keep<0x143, 0xc>(x));  // row_bcast 31
+    return x;
+}
+
+// Each wave finds its workgroup's item. Offsets are clamped into [0, T] and
+// made non-decreasing (a running maximum), 64 sequences at a time.
+__device__ __forceinline__ LinItem lin_item(const LinWork &w, int item, int lane) {
+    auto clampT = [&](int x) { return min(max(x, 0), w.total_tokens); };
+    int carry = clampT(w.cu[0]);  // where sequence `base` starts
+    int lo = 0, hi = 0, seq = -1;
+    for (int base = 0; base < w.num_seqs; base += 64) {
+        const int n = base + lane;
+        int e = n < w.num_seqs ? clampT(w.cu[n + 1]) : 0;
+        e = wave_scan_max(max(e, carry));        // where sequence n ends
+        // and starts (the move stands alone: every lane has to take part in it)
+        const int before = __builtin_amdgcn_update_dpp(carry, e, 0x138, 0xf, 0xf, false);  // wave_shr 1
+        const int s = lane == 0 ? carry : before;
+        const int first = w.seg_shift < 0 ? n : (s >> w.seg_shift) + n;
+        const uint64_t at = __ballot(n < w.num_seqs && first <= item);
+        if (at) {
+            const int l = 63 - __builtin_clzll(at);
+            seq = base + l;
+            lo = __builtin_amdgcn_readlane(s, l);
+            hi = __builtin_amdgcn_readlane(e, l);
+        }
+        carry = __builtin_amdgcn_readlane(e, 63);
+        if (at != ~0ull) break;
+    }
+    LinItem r;
+    r.seq = seq;
+    r.none = seq < 0;
+    r.seg = 0;
+    r.segs = 1;
+    r.lo = lo;
+    r.hi = hi;
+    if (w.seg_shift >= 0) {
+        const int len = hi - lo, L = 1 << w.seg_shift;
+        r.seg = item - ((lo >> w.seg_shift) + seq);
+        r.segs = max(1, (int)(((uint32_t)len + (uint32_t)L - 1u) >> w.seg_shift));
+        r.none = r.none || r.seg >= r.segs;
+        const int off = r.none ? 0 : r.seg << w.seg_shift;
+        r.lo = lo + off;
+        r.hi = lo + off + min(len - off, L);
+    }
+    return r;
+}
+
+// Workgroups go to the XCDs in turn. The heads that share a key head's
+// items sit eight apart, on one XCD, whose L2 then reads their q and k once.
+__device__ __forceinline__ bool lin_place(const LinWork &w, uint32_t &item, uint32_t &kh, uint32_t &h) {
+    const uint32_t x = blockIdx.x & 7, m = blockIdx.x >> 3;
+    const uint32_t r = m / w.group, u = x + 8 * r;
+    item = u / w.hk;
+    kh = u - item * w.hk;
+    h = kh * w.group + (m - r * w.group);
+    return u < w.units;
+}
+inline int64_t lin_grid(int64_t units, int64_t group) { return (units + 7) / 8 * 8 * group; }
+
+// ------------------------------------------------------------- the kernel
+
+struct LinIo {
+    const void *q, *k, *v, *g;
+    int64_t gate_ld;  // elements of g from a token to the next
+    const void *s0;
+    void *s_final;
+    void *out;
+    float *seg_state;  // [item][hv] states of segments, accumulator order
+    float *seg_decay;  // [item][hv]
+    float scale;
+    bool gate_bf16, state_bf16;
+};
+
+template <typename E, int DK, int DV> struct LinShape {
+    static constexpr int C = std::is_same<E, bf16>::value ? 64 : 32;  // tokens per chunk
+    static constexpr int NW = DV >= 64 ? 4 : DV / 16, THREADS = 64 * NW;
+    static constexpr int NT = DV / 16 / NW;                           // 16-column tiles of dv per wave
+    static constexpr int WPS = NW == 4 ? 2 : 1;                       // waves per SIMD to fit
+    static constexpr int MT = DK / 16;                                // 16-row tiles of dk
+    typedef LinOp<E, DK> OK;                                          // contractions over dk
+    typedef LinOp<E, C> OT;                                           // contractions over tokens
+    static constexpr int KB = DK / OK::KW, TB = C / OT::KW;           // steps of each
+    // LDS rows, elements. With rows 32 bytes off a multiple of 256 fragment
+    // reads (16 bytes from each of 16 rows) and transposing reads (32 bytes
+    // from each of 16) are free of bank conflicts: 213 and 167 bytes a clock,
+    // 120 and 123 with rows 16 bytes off.
+    static constexpr int PAD = 32 / (int)sizeof(E);
+    static constexpr int LDK = DK + PAD, LDV = DV + PAD, LDP = C + PAD;
+};
+
+// Rows of a chunk between global memory, registers and LDS, 16-byte pieces:
+// thread tid takes the same piece of every STEP-th row. A whole chunk's
+// addresses are one register beside uniform ones; a last chunk of fewer `rows`
+// reads its last row again in place of the missing ones and stores zeros.
+template <typename E, int D, int C, int THREADS> struct LinStage {
+    static constexpr int PIECE = 16 / (int)sizeof(E), PPR = D / PIECE, STEP = THREADS / PPR, N = C > STEP ? C / STEP : 1;
+    static_assert(THREADS % PPR == 0 && (C % STEP == 0 || STEP > C), "whole rows per step");
+    Vec16 r[N];
+    uint32_t at;  // bytes from the chunk's first row
+    __device__ __forceinline__ void init(size_t ld, int tid) {
+        at = (uint32_t)((min(tid / PPR, C - 1) * ld + tid % PPR * PIECE) * sizeof(E));
+    }
+    __device__ __forceinline__ void load(const E *src, size_t ld, int rows, int tid) {
+        if (rows >= C) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                r[i] = ld16(reinterpret_cast<const char *>(src + (size_t)(i * STEP) * ld) + at);
+        } else {
+            asm volatile("" : "+v"(tid));
+            const int row = tid / PPR, piece = tid % PPR * PIECE;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                r[i] = ld16(src + (size_t)min(row + i * STEP, rows - 1) * ld + piece);
+        }
+    }
+    __device__ __forceinline__ void store(E *dst, int ld, int rows, int tid) {
+        asm volatile("" : "+v"(tid));
+        const int row = tid / PPR, piece = tid % PPR * PIECE;
+        if (STEP > C && row >= C) return;
+        E *d = dst + row * ld + piece;
+#pragma unroll
+        for (int i = 0; i < N; ++i) st16(d + i * STEP * ld, r[i]);
+        if (rows < C) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (row + i * STEP >= rows) st16(d + i * STEP * ld, zero16());
+        }
+    }
+};
+
+// Inclusive sums over the wave's lanes on DPP moves: within rows of 16, then
+// rows 1 and 3 take row 0's and 2's last, then lanes 32 .. 63 lane 31's.
+template <int Ctrl, int RowMask> __device__ __forceinline__ double dpp_add_f64(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, Ctrl, RowMask, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), Ctrl, RowMask, 0xf, false);
+    return x + __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+__device__ __forceinline__ double wave_scan_f64(double x) {
+    x = dpp_add_f64<0x111, 0xf>(x);  // row_shr 1
+    x = dpp_add_f64<0x112, 0xf>(x);
+    x = dpp_add_f64<0x114, 0xf>(x);
+    x = dpp_add_f64<0x118, 0xf>(x);
+    x = dpp_add_f64<0x142, 0xa>(x);  // row_bcast 15
+    x = dpp_add_f64<0x143, 0xc>(x);  // row_bcast 31
+    return x;
+}
+__device__ __forceinline__ double lane_f64(double x, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, l);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+
+__device__ __forceinline__ float gate_value(uint32_t bits, bool is_bf16) {
+    return __builtin_bit_cast(float, is_bf16 ? bits << 16 : bits);
+}
+// A gate in units of log 2, at least -1024: exp of anything lower is 0 in fp32
+// as well, and a difference of two sums stays a number after exp(g) = 0.
+__device__ __forceinline__ double gate_log2(float g) { return fmax((double)g * 1.4426950408889634, -1024.0); }
+
+// x as the sum of three bf16 numbers.
+struct Split3 { bf16 hi, mid, lo; };
+__device__ __forceinline__ Split3 split3(float x) {
+    Split3 s;
+    s.hi = static_cast<bf16>(x);
+    const float r1 = x - static_cast<float>(s.hi);
+    s.mid = static_cast<bf16>(r1);
+    s.lo = static_cast<bf16>(r1 - static_cast<float>(s.mid));
+    return s;
+}
+
+// What a launch computes. kLinWhole: outputs and final states of whole
+// sequences. Split: kLinSegState, the state at the end of each segment as if
+// it began from zero (the first one from the initial state), and its decay;
+// then, joined, kLinSegOut, the outputs from the states before each segment,
+// and the final states. The state that kLinSegOut carries from chunk to chunk
+// only goes into outputs, so two parts of delta v, 16 bits, are enough there.
+enum LinMode { kLinWhole, kLinSegState, kLinSegOut };
+
+//
+// A chunk goes in two steps with a barrier after each, each with as much
+// independent work as there is, for the waves of a CU wait on latencies far
+// more than on any unit:
+//   1. scores of the wave's tiles, to LDS; S0 q; the new state
+//   2. P v and the stores; the next chunk, on its way since step 1, to LDS
+// (step 2 reads the scores only: v's columns are in registers by then).
+template <typename E, int DK, int DV, LinMode kMode>
+__global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV>::WPS)) void gdn_linattn_chunk_kernel(
+    LinWork w, LinIo io)
+{
+    typedef LinShape<E, DK, DV> SH;
+    typedef typename SH::OK OK;
+    typedef typename SH::OT OT;
+    constexpr int C = SH::C, TT = C / 16, MT = SH::MT, KB = SH::KB, TB = SH::TB, THREADS = SH::THREADS, NW = SH::NW,
+                  NT = SH::NT, LDK = SH::LDK, LDV = SH::LDV, LDP = SH::LDP;
+    constexpr bool kBf16 = std::is_same<E, bf16>::value;
+    constexpr bool kOut = kMode != kLinSegState;
+    constexpr int kParts = !kBf16 ? 1 : kMode == kLinSegOut ? 2 : 3;  // parts of delta v
+    constexpr int kColStride = OK::KPL == 8 ? 8 : 4;                  // of k's columns in a tile, see tile_base
+
+    __shared__ __attribute__((aligned(16))) E s_q[kOut ? C * LDK : 8];
+    __shared__ __attribute__((aligned(16))) E s_k[C * LDK];
+    __shared__ __attribute__((aligned(16))) E s_v[C * LDV];
+    __shared__ __attribute__((aligned(16))) E s_p[kOut ? C * LDP : 8];
+    __shared__ __attribute__((aligned(16))) float s_chi[C], s_clo[C], s_gamma[C], s_delta[C];
+    __shared__ float s_total;
+
+    const int tid = threadIdx.x, lane0 = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = lane0, m = lane & 15, g = lane >> 4;
+
+    uint32_t item, kh, h;
+    if (!lin_place(w, item, kh, h)) return;
+    const LinItem it = lin_item(w, (int)item, lane);
+    if (it.none) return;
+    const int hv = (int)(w.hk * w.group);
+
+    const E *q = (const E *)io.q + (size_t)kh * DK, *k = (const E *)io.k + (size_t)kh * DK,
+            *v = (const E *)io.v + (size_t)h * DV;
+    const size_t ldk = (size_t)w.hk * DK, ldv = (size_t)hv * DV;
+    LinStage<E, DK, C, THREADS> rq, rk;
+    LinStage<E, DV, C, THREADS> rv;
+    rq.init(ldk, tid);
+    rk.init(ldk, tid);
+    rv.init(ldv, tid);
+    uint32_t rg = 0;  // the gate's bits: converting them here would wait for the load
+    auto load = [&](int t0) {
+        const int rows = min(it.hi - t0, C);
+        if constexpr (kOut) rq.load(q + (size_t)t0 * ldk, ldk, rows, tid);
+        rk.load(k + (size_t)t0 * ldk, ldk, rows, tid);
+        rv.load(v + (size_t)t0 * ldv, ldv, rows, tid);
+        if (wave == NW - 1) {
+            const size_t ga = (size_t)(t0 + min(lane, rows - 1)) * io.gate_ld + h;
+            rg = io.gate_bf16 ? ((const uint16_t *)io.g)[ga] : ((const uint32_t *)io.g)[ga];
+        }
+    };
+    double decay = 0.0;  // of the whole segment, log 2 (last wave)
+    auto stage = [&](int t0) {
+        const int rows = min(it.hi - t0, C);
+        if (wave == NW - 1) {
+            const double c = wave_scan_f64(lane < rows ? gate_log2(gate_value(rg, io.gate_bf16)) : 0.0);
+            const double total = lane_f64(c, C - 1);
+            if (lane < C) {
+                const float hi = (float)c;
+                s_chi[lane] = hi;
+                s_clo[lane] = (float)(c - (double)hi);
+                s_gamma[lane] = io.scale * __builtin_amdgcn_exp2f((float)c);
+                s_delta[lane] = __builtin_amdgcn_exp2f((float)(total - c));
+            }
+            if (lane == 0) s_total = __builtin_amdgcn_exp2f((float)total);
+            decay += total;
+        }
+        if constexpr (kOut) rq.store(s_q, LDK, rows, tid);
+        rk.store(s_k, LDK, rows, tid);
+        rv.store(s_v, LDV, rows, tid);
+    };
+    // The first chunk's loads go out before the state's: they are waited for first.
+    if (it.lo < it.hi) load(it.lo);
+
+    // This lane's part of the state: tile (mt, nt) holds dk dk_of(mt) .. + 3 of
+    // column dv_of(nt). Two tiles' columns alternate in fours, so that a
+    // lane's outputs of one token are 4 NT consecutive dv.
+    constexpr int kTiles = MT * NT, kVStride = 4 * NT;
+    const int dv0 = 16 * NT * wave;
+    auto dk_of = [&](int t) { return tile_base<OK>(t / NT) + OK::KPL * g; };
+    auto dv_of = [&](int t) { return dv0 + kVStride * (m >> 2) + 4 * (t % NT) + (m & 3); };
+    f32x4 S[kTiles];
+    const size_t seg_at = ((size_t)item * hv + h) * (DK * DV) + tid * 4;
+    const size_t state_at = ((size_t)it.seq * hv + h) * (DK * DV);
+    if (kOut && it.seg > 0) {
+        const float *src = io.seg_state + seg_at - (size_t)hv * (DK * DV);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) S[t] = *reinterpret_cast<const f32x4 *>(src + t * THREADS * 4);
+    } else if (io.s0 && it.seg == 0) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const size_t at = state_at + (size_t)dv_of(t) * DK + dk_of(t);
+            S[t] = io.state_bf16 ? load4f<bf16>((const bf16 *)io.s0 + at) : load4f<float>((const float *)io.s0 + at);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    if (it.lo < it.hi) stage(it.lo);
+    for (int t0 = it.lo; t0 < it.hi; t0 += C) {
+        const bool more = t0 + C < it.hi;
+        if (more) load(t0 + C);
+        __syncthreads();
+
+        // ---- step 1
+        int lane_ = lane0;
+        asm volatile("" : "+v"(lane_));
+        const int lane = lane_, m = lane & 15, g = lane >> 4, g4 = 4 * g;
+        typename OT::Frag fv[TB * NT];
+#pragma unroll
+        for (int t = 0; t < TB * NT; ++t)
+            fv[t] = col_frag<OT>(s_v, LDV, t / NT, dv0 + 4 * (t % NT), kVStride, lane);
+
+        f32x4 o[kOut ? TT * NT : 1];
+        if constexpr (kOut) {
+            // Scores P^T = K Q^T, tiles (tokens j, tokens i). A product's
+            // contraction steps reach kStep tiles, past the diagonal too:
+            // row I has the tiles of its last step, (I / kStep + 1) kStep,
+            // those above the diagonal zero. Tile number u of the list
+            // (0,0), .. goes to wave u % NW.
+            constexpr int kStep = OT::KW / 16, kScores = TT * (TT + kStep) / 2, kMine = (kScores + NW - 1) / NW,
+                          kSide = kMine < 3 ? kMine : 3;
+#pragma unroll
+            for (int r = 0; r < kMine; r += kSide) {
+                f32x4 p[kSide];
+                int I[kSide], J[kSide];
+#pragma unroll
+                for (int s = 0; s < kSide; ++s) {
+                    // (a wave past the list's end repeats the last tile)
+                    const int u = min((r + s) * NW + wave, kScores - 1);
+                    if constexpr (kStep == 2) {  // rows of 2, 2, 4, 4 tiles
+                        I[s] = u < 4 ? u >> 1 : 2 + ((u - 4) >> 2);
+                        J[s] = u < 4 ? u & 1 : (u - 4) & 3;
+                    } else {                     // rows of 1, 2 tiles
+                        I[s] = u > 0;
+                        J[s] = u >> 1;
+                    }
+                    p[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int s = 0; s < kSide; ++s)
+                        p[s] = OK::mma(row_frag<OK>(s_k, LDK, 16 * J[s], kb, lane),
+                                       row_frag<OK>(s_q, LDK, 16 * I[s], kb, lane), p[s]);
+#pragma unroll
+                for (int s = 0; s < kSide; ++s) {
+                    const int i = 16 * I[s] + m, j0 = 16 * J[s] + g4;
+                    const float hi = s_chi[i], lo = s_clo[i];
+                    const f32x4 jhi = *reinterpret_cast<const f32x4 *>(s_chi + j0),
+                                jlo = *reinterpret_cast<const f32x4 *>(s_clo + j0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // (exp2 of -16384 is 0)
+                        const float x = j0 + e <= i ? (hi - jhi[e]) + (lo - jlo[e]) : -16384.f;
+                        p[s][e] *= io.scale * __builtin_amdgcn_exp2f(x);
+                    }
+                    store4<E>(s_p + i * LDP + frag_pos<OT>(j0), p[s]);
+                }
+            }
+            GDN_SCHED_BARRIER();
+#pragma unroll
+            for (int t = 0; t < TT * NT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                if (kb % 2 == 0) GDN_SCHED_BARRIER();
+                typename OK::Frag fs[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    f32x4 col[MT];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) col[mt] = S[mt * NT + nt];
+                    fs[nt] = acc_frag<OK, E>(col, kb);
+                }
+#pragma unroll
+                for (int I = 0; I < TT; ++I) {
+                    const typename OK::Frag fq = row_frag<OK>(s_q, LDK, 16 * I, kb, lane);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] = OK::mma(fs[nt], fq, o[I * NT + nt]);
+                }
+            }
+#pragma unroll
+            for (int I = 0; I < TT; ++I) {
+                const float gamma = s_gamma[16 * I + m];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] *= gamma;
+            }
+        }
+
+        GDN_SCHED_BARRIER();
+        if (kMode != kLinSegOut || more) {
+            // S^T <- gamma_C S^T + K^T (delta V)
+            const float total = s_total;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) S[t] *= total;
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) {
+                GDN_SCHED_BARRIER();
+                typename OT::Frag vd[NT][kParts];
+#pragma unroll
+                for (int u = 0; u < OT::KPL / 4; ++u) {
+                    const f32x4 d = *reinterpret_cast<const f32x4 *>(s_delta + tb * OT::KW + 16 * u + g4);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = d[e] * to_f32(fv[tb * NT + nt][4 * u + e]);
+                            if constexpr (kBf16) {
+                                const Split3 s = split3(x);
+                                vd[nt][0][4 * u + e] = s.hi;
+                                vd[nt][1][4 * u + e] = s.mid;
+                                if constexpr (kParts == 3) vd[nt][2][4 * u + e] = s.lo;
+                            } else {
+                                vd[nt][0][4 * u + e] = x;
+                            }
+                        }
+                }
+                // Two tiles of dk at a time, so that a product does not follow
+                // on the one it adds to.
+                constexpr int kSide = MT < 2 ? 1 : 2;
+#pragma unroll
+                for (int mt = 0; mt < MT; mt += kSide) {
+                    typename OT::Frag fk[kSide];
+#pragma unroll
+                    for (int s = 0; s < kSide; ++s)
+                        fk[s] = col_frag<OT>(s_k, LDK, tb, tile_base<OK>(mt + s), kColStride, lane);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                        for (int s = 0; s < kSide; ++s)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                S[(mt + s) * NT + nt] = OT::mma(fk[s], vd[nt][part], S[(mt + s) * NT + nt]);
+                }
+            }
+        }
+        __syncthreads();
+
+        // ---- step 2
+        if constexpr (kOut) {
+            constexpr int kStep = OT::KW / 16;
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+#pragma unroll
+                for (int I = b * kStep; I < TT; ++I) {
+                    const typename OT::Frag fp = row_frag<OT>(s_p, LDP, 16 * I, b, lane);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] = OT::mma(fv[b * NT + nt], fp, o[I * NT + nt]);
+                }
+        }
+        GDN_SCHED_BARRIER();
+        if (more) stage(t0 + C);
+        GDN_SCHED_BARRIER();
+        if constexpr (kOut) {
+            E *dst = (E *)io.out + (size_t)t0 * ldv + (size_t)h * DV + dv0 + kVStride * g;
+#pragma unroll
+            for (int I = 0; I < TT; ++I)
+                if (16 * I + m < it.hi - t0) {
+                    E *row = dst + (size_t)(16 * I + m) * ldv;
+                    if constexpr (kBf16 && NT == 2) {
+                        bf16x8 x;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = static_cast<bf16>(o[I * NT + (e >> 2)][e & 3]);
+                        *reinterpret_cast<bf16x8 *>(row) = x;
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) store4<E>(row + 4 * nt, o[I * NT + nt]);
+                    }
+                }
+        }
+    }
+
+    if constexpr (kMode == kLinSegState) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4 *>(io.seg_state + seg_at + t * THREADS * 4) = S[t];
+        if (tid == THREADS - 64) io.seg_decay[(size_t)item * hv + h] = __builtin_amdgcn_exp2f((float)decay);
+    } else if (io.s_final && it.seg == 0) {
+        // Split: the joined state of the last segment, stored by the
+        // workgroup that has read the initial state, which may be the same
+        // buffer.
+        const float *joined = io.seg_state + seg_at + (size_t)(it.segs - 1) * hv * (DK * DV);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const size_t at = state_at + (size_t)dv_of(t) * DK + dk_of(t);
+            const f32x4 x = kMode == kLinWhole ? S[t] : *reinterpret_cast<const f32x4 *>(joined + t * THREADS * 4);
+            if (io.state_bf16) store4<bf16>((bf16 *)io.s_final + at, x);
+            else store4<float>((float *)io.s_final + at, x);
+        }
+    }
+}
+
+// Joins the segments of a sequence: each segment's state becomes the state at
+// its end, S_s = decay_s S_{s-1} + local_s. One lane per four elements; the
+// chain over segments is a multiply-add each, the loads run ahead of it.
+template <int DK, int DV>
+__global__ __launch_bounds__(256) void gdn_linattn_join_kernel(LinWork w, LinIo io)
+{
+    constexpr int kQuads = DK * DV / 4, kBlocks = (kQuads + 255) / 256, kAhead = 8;
+    const int lane = threadIdx.x & 63;
+    const int hv = (int)(w.hk * w.group);
+    const int block = blockIdx.x % kBlocks, nh = blockIdx.x / kBlocks;
+    const int n = nh / hv, h = nh - n * hv;
+    // the sequence's bounds, as lin_item finds them
+    auto clampT = [&](int x) { return min(max(x, 0), w.total_tokens); };
+    int lo = clampT(w.cu[0]), hi = lo;
+    for (int j = lane; j <= n; j += 64) {
+        const int e = clampT(w.cu[j + 1]);
+        hi = max(hi, e);
+        if (j < n) lo = max(lo, e);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        hi = max(hi, __shfl_xor(hi, off));
+        lo = max(lo, __shfl_xor(lo, off));
+    }
+    const int segs = (int)(((uint32_t)(hi - lo) + (1u << w.seg_shift) - 1u) >> w.seg_shift);
+    const int item0 = (lo >> w.seg_shift) + n;
+    const int quad = block * 256 + threadIdx.x;
+    if (quad >= kQuads) return;
+    float *at = io.seg_state + ((size_t)item0 * hv + h) * (DK * DV) + (size_t)quad * 4;
+    const float *dec = io.seg_decay + (size_t)item0 * hv + h;
+    const size_t ld = (size_t)hv * (DK * DV);
+    f32x4 S = *reinterpret_cast<const f32x4 *>(at);
+    for (int s0 = 1; s0 < segs; s0 += kAhead) {
+        f32x4 x[kAhead];
+        float d[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int s = min(s0 + u, segs - 1);
+            x[u] = *reinterpret_cast<const f32x4 *>(at + s * ld);
+            d[u] = dec[(size_t)s * hv];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (s0 + u >= segs) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[e] = __builtin_fmaf(d[u], S[e], x[u][e]);
+            *reinterpret_cast<f32x4 *>(at + (s0 + u) * ld) = S;
+        }
+    }
+}
+
+}  // namespace gdn

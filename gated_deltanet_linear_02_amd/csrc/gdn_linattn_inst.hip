@@ -1,0 +1,54 @@
+// gdn_linattn_inst.hip -- one (element type, dk) instantiation of the chunked
+// linear attention (gdn_linattn_chunk.hpp), for every dv. The build compiles
+// this file once per pair, with GDN_INST_BF16 (1: bf16 I/O, 0: fp32 I/O) and
+// GDN_INST_DK defined, so that they compile in parallel.
+#include "gdn_linattn_chunk.hpp"
+
+// Compiled without the two macros the file is empty.
+#if defined(GDN_INST_BF16) && defined(GDN_INST_DK)
+
+namespace gdn {
+
+#if GDN_INST_BF16
+typedef bf16 InstElem;
+#else
+typedef float InstElem;
+#endif
+
+template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinPrefillArgs &A, hipStream_t st) {
+    typedef LinShape<E, DK, DV> SH;
+    const uint32_t hk = (uint32_t)A.hk, group = (uint32_t)(A.hv / A.hk);
+    const LinWork w{A.cu, A.num_seqs, (int32_t)A.total_tokens, A.plan.seg_shift, hk, group,
+                    (uint32_t)A.plan.items * hk};
+    LinIo io;
+    io.q = A.q; io.k = A.k; io.v = A.v; io.g = A.g; io.gate_ld = A.gate_per_head ? 0 : A.hv;
+    io.s0 = A.s0; io.s_final = A.s_final; io.out = A.out; io.scale = A.scale;
+    io.gate_bf16 = A.gate_bf16; io.state_bf16 = A.state_bf16;
+    io.seg_state = reinterpret_cast<float *>(A.ws + A.plan.off_state);
+    io.seg_decay = reinterpret_cast<float *>(A.ws + A.plan.off_decay);
+    const dim3 grid((unsigned)lin_grid(w.units, group)), block(SH::THREADS);
+    auto launch = [&](KernelKind kind, auto mode) {
+        return launch_kernel(kind, gdn_linattn_chunk_kernel<E, DK, DV, mode()>, grid, block, 0, st, w, io);
+    };
+    if (w.seg_shift < 0) return launch(kLinOut, std::integral_constant<LinMode, kLinWhole>());
+    hipError_t e = launch(kLinState, std::integral_constant<LinMode, kLinSegState>());
+    if (e != hipSuccess) return e;
+    const unsigned blocks = (unsigned)A.num_seqs * (unsigned)A.hv * ((DK * DV / 4 + 255) / 256);
+    e = launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV>, dim3(blocks), dim3(256), 0, st, w, io);
+    if (e != hipSuccess) return e;
+    return launch(kLinOut, std::integral_constant<LinMode, kLinSegOut>());
+}
+
+template <> hipError_t launch_linattn_chunk_k<GDN_INST_BF16, GDN_INST_DK>(const LinPrefillArgs &A, hipStream_t st) {
+    switch (A.dv) {
+    case 16: return launch_linattn_chunk<InstElem, GDN_INST_DK, 16>(A, st);
+    case 32: return launch_linattn_chunk<InstElem, GDN_INST_DK, 32>(A, st);
+    case 64: return launch_linattn_chunk<InstElem, GDN_INST_DK, 64>(A, st);
+    case 128: return launch_linattn_chunk<InstElem, GDN_INST_DK, 128>(A, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace gdn
+
+#endif
