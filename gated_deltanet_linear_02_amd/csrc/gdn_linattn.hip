@@ -7,6 +7,9 @@
 // subtracted along k, so every row of S is scaled and added to, and the
 // output of the new state is scale (a (S q) + v (k.q)) over the old one.
 #include "gdn_linattn.hpp"
+
+#include <cmath>
+
 #include "gdn_rows.hpp"
 
 namespace gdn {
@@ -175,20 +178,69 @@ hipError_t launch_linattn_decode(const LinDecodeArgs &A, hipStream_t st) {
 // Prefill
 // ---------------------------------------------------------------------------
 
-// Sequences are cut where whole ones would leave compute units idle.
-LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv) {
-    constexpr int64_t kWorkgroups = 512, kLeast = 256;
-    LinPlan P;
+// How a prefill is split, by an estimate of its time (us). Workgroups run in
+// rounds of two per compute unit; one takes a fixed time and one per chunk of
+// its segment, less with a unit to itself. States of 128 rows may go as two of
+// 64: half the work per workgroup, but the scores are formed twice. Segments cost
+// a pass for their states, the joining (memory, and a chain over a sequence's
+// segments) and two more launches. Fitted at HK = 16, HV = 32, d = 128 and 64 to
+// 1 x 512 .. 16,384 and 8 x 512 tokens; measured there (all kernels, us):
+//   1 x 512     two of 64 rows: whole 26.4, segments of 128: 27.3, of 64: 27.9
+//   1 x 1,024   two of 64: segments of 128 33.1, of 256 34.2; one: of 128 38.2
+//   1 x 2,048   two of 64: of 256 44.0; one: of 256 49.3
+//   1 x 4,096   two of 64: of 512 63.9; one: of 256 66.2, of 512 70.5
+//   1 x 16,384  one: of 1,024 174, of 512 195; two of 64: of 1,024 202
+//   8 x 512     one: whole 39.7, of 256 75.4; two of 64: whole 41.4
+LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv,
+                     bool io_bf16) {
+    const double chunk = io_bf16 ? 64 : 32, cus = 256;
+    const double N = (double)num_seqs, T = (double)total_tokens;
+    // Without a hint the longest sequence may be all there is.
+    const double longest = max_seqlen ? (double)max_seqlen : T, mean = T / N;
+    LinPlan best;
+    double best_t = 0;
+    auto consider = [&](int32_t dv_shift, int32_t seg_shift) {
+        const bool wide = (dv >> dv_shift) == 128;
+        const double heads = (double)(hv << dv_shift);
+        const bool split = seg_shift >= 0;
+        const double L = split ? (double)((int64_t)1 << seg_shift) : 0;
+        const double items = split ? T / L + (num_seqs > 1 ? 0.5 * N : 0) : N;
+        const double wgs = items * heads;
+        // per chunk: outputs, states; with a unit to itself and with a second workgroup
+        const double out1 = wide ? 3.2 : 2.0, out2 = wide ? 5.4 : 3.4, st1 = wide ? 2.0 : 1.3, st2 = wide ? 3.5 : 1.7;
+        const double rounds = std::max(1.0, wgs / (2 * cus));
+        const double full = std::min(1.0, std::max(0.0, wgs / cus - 1.0));  // units with two
+        auto pass = [&](double fixed, double one, double two, double tokens, double most) {
+            const double step = one + full * (two - one);
+            // the longest workgroup may outlast the rounds of the others
+            return std::max(rounds * (fixed + std::ceil(tokens / chunk) * step), fixed + std::ceil(most / chunk) * one);
+        };
+        double t;
+        if (split) {
+            const double seg = std::min(L, longest), segs = std::ceil(longest / L);
+            t = pass(9.5, out1, out2, seg, seg) + pass(7.5, st1, st2, seg, seg) + 4 + 4 +
+                items * (double)hv * (double)(dk * dv) * 8 / 6e6 + 0.11 * segs;
+        } else {
+            t = pass(9, 1.35 * out1, 1.35 * out2, mean, longest);
+        }
+        if (best_t == 0 || t < best_t) {
+            best_t = t;
+            best.dv_shift = dv_shift;
+            best.seg_shift = seg_shift;
+        }
+    };
+    for (int32_t f = 0; f <= (dv == 128 ? 1 : 0); ++f) {
+        consider(f, -1);
+        for (int32_t s = 6; ((int64_t)1 << s) < total_tokens && s < 31; ++s) consider(f, s);
+    }
+    LinPlan P = best;
     P.items = num_seqs;
-    const int64_t longest = max_seqlen ? max_seqlen : total_tokens;
-    int shift = 6;
-    while ((int64_t)1 << shift < kLeast || ((int64_t)kWorkgroups << shift) < total_tokens * hv) ++shift;
-    if (longest <= (int64_t)1 << shift) return P;
-    P.seg_shift = shift;
-    P.items = (total_tokens >> shift) + num_seqs;
-    P.off_state = 0;
-    P.off_decay = align256((size_t)P.items * hv * dk * dv * sizeof(float));
-    P.total = align256(P.off_decay + (size_t)P.items * hv * sizeof(float));
+    if (P.seg_shift >= 0) {
+        P.items = (total_tokens >> P.seg_shift) + num_seqs;
+        P.off_state = 0;
+        P.off_decay = align256((size_t)P.items * hv * dk * dv * sizeof(float));
+        P.total = align256(P.off_decay + (size_t)P.items * (hv << P.dv_shift) * sizeof(float));
+    }
     return P;
 }
 

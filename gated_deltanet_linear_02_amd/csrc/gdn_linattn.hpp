@@ -11,12 +11,14 @@ namespace gdn {
 // 2^seg_shift tokens whose states go through the workspace.
 struct LinPlan {
     int32_t seg_shift = -1;
+    int32_t dv_shift = 0;       // a state of dv rows goes as 2^dv_shift states of fewer
     int64_t items = 0;          // sequences, or the bound on segments
     size_t off_state = 0;       // float [items][hv][dv * dk], accumulator order
-    size_t off_decay = 0;       // float [items][hv]
+    size_t off_decay = 0;       // float [items][hv << dv_shift]
     size_t total = 0;           // bytes of workspace
 };
-LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv);
+LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv,
+                     bool io_bf16);
 
 struct LinPrefillArgs {
     const void *q, *k, *v, *g;

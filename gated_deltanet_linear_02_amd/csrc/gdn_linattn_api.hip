@@ -29,9 +29,11 @@ static int32_t check_linattn_prefill(int32_t num_seqs, int64_t total_tokens, int
     if (max_seqlen != 0 &&
         (max_seqlen < 0 || max_seqlen > total_tokens || max_seqlen * (int64_t)num_seqs < total_tokens))
         return GDN_ERR_BAD_VALUE;
+    // A chunk's rows lie within 32 bits of each other (LinStage).
     // The grids: items (segments, or sequences) x heads, 64 workgroups of the
     // join per (sequence, head) at most.
     const int64_t items = total_tokens / 64 + num_seqs + 8;
+    if ((int64_t)hv * dv > (int64_t)1 << 22 || (int64_t)hk * dk > (int64_t)1 << 22) return GDN_ERR_UNSUPPORTED;
     if ((double)items * hv > INT32_MAX || (double)num_seqs * hv * 64 > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
@@ -43,7 +45,7 @@ size_t gdn_linattn_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens
     if (check_linattn_prefill(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv, io_dtype, GDN_F32, 0, GDN_F32) !=
         GDN_OK)
         return 0;
-    return std::max<size_t>(256, linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv).total);
+    return std::max<size_t>(256, linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv, io_dtype == GDN_BF16).total);
 }
 
 int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const void *g, const int32_t *cu_seqlens,
@@ -59,7 +61,7 @@ int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const v
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(initial_state) ||
         !aligned16(final_state))
         return GDN_ERR_MISALIGNED;
-    const LinPlan plan = linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv);
+    const LinPlan plan = linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv, io_dtype == GDN_BF16);
     const size_t used = plan.total;
     if (used && (!workspace || workspace_bytes < used || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return GDN_ERR_WORKSPACE;

@@ -75,6 +75,7 @@ __device__ __forceinline__ typename OP::Frag row_frag(const E *base, int ld, int
                                                         OP::KPL * (lane >> 4));
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 LdsQuad;
 
 // Four tokens of one column. Lane (m, g) gets rows t0 + 4 g .. + 3 of column
@@ -211,7 +212,8 @@ inline int64_t lin_grid(int64_t units, int64_t group) { return (units + 7) / 8 *
 
 struct LinIo {
     const void *q, *k, *v, *g;
-    int64_t gate_ld;  // elements of g from a token to the next
+    int64_t gate_ld;     // elements of g from a token to the next
+    int32_t gate_shift;  // value head h of the launch has gate h >> gate_shift
     const void *s0;
     void *s_final;
     void *out;
@@ -238,43 +240,37 @@ template <typename E, int DK, int DV> struct LinShape {
     static constexpr int LDK = DK + PAD, LDV = DV + PAD, LDP = C + PAD;
 };
 
+// A chunk's rows of one head in global memory, as a buffer: rows from `rows`
+// on lie past its end, so that they read as zeros and are not written, by the
+// hardware's range check. Row distances fit 32 bits (64 rows of at most 2^22
+// elements, checked on the host).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const void *first, uint32_t row_bytes, int rows,
+                                                             uint32_t used_bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0,
+                                             (int)((uint32_t)(rows - 1) * row_bytes + used_bytes), 0x00027000);
+}
+
 // Rows of a chunk between global memory, registers and LDS, 16-byte pieces:
-// thread tid takes the same piece of every STEP-th row. A whole chunk's
-// addresses are one register beside uniform ones; a last chunk of fewer `rows`
-// reads its last row again in place of the missing ones and stores zeros.
+// thread tid takes the same piece of every STEP-th row.
 template <typename E, int D, int C, int THREADS> struct LinStage {
     static constexpr int PIECE = 16 / (int)sizeof(E), PPR = D / PIECE, STEP = THREADS / PPR, N = C > STEP ? C / STEP : 1;
     static_assert(THREADS % PPR == 0 && (C % STEP == 0 || STEP > C), "whole rows per step");
-    Vec16 r[N];
-    uint32_t at;  // bytes from the chunk's first row
-    __device__ __forceinline__ void init(size_t ld, int tid) {
-        at = (uint32_t)((min(tid / PPR, C - 1) * ld + tid % PPR * PIECE) * sizeof(E));
-    }
-    __device__ __forceinline__ void load(const E *src, size_t ld, int rows, int tid) {
-        if (rows >= C) {
+    u32x4 r[N];
+    __device__ __forceinline__ void load(const E *first, uint32_t row_bytes, int rows, int tid) {
+        const __amdgpu_buffer_rsrc_t rsrc = chunk_rows(first, row_bytes, min(rows, C), D * (uint32_t)sizeof(E));
+        asm volatile("" : "+v"(tid));  // addresses formed here, not kept in registers over the loop
+        const uint32_t at = (uint32_t)(tid / PPR) * row_bytes + (uint32_t)(tid % PPR) * 16u;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                r[i] = ld16(reinterpret_cast<const char *>(src + (size_t)(i * STEP) * ld) + at);
-        } else {
-            asm volatile("" : "+v"(tid));
-            const int row = tid / PPR, piece = tid % PPR * PIECE;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                r[i] = ld16(src + (size_t)min(row + i * STEP, rows - 1) * ld + piece);
-        }
+        for (int i = 0; i < N; ++i)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)(at + (uint32_t)(i * STEP) * row_bytes), 0, 0);
     }
-    __device__ __forceinline__ void store(E *dst, int ld, int rows, int tid) {
+    __device__ __forceinline__ void store(E *dst, int ld, int tid) {
         asm volatile("" : "+v"(tid));
-        const int row = tid / PPR, piece = tid % PPR * PIECE;
+        const int row = tid / PPR;
         if (STEP > C && row >= C) return;
-        E *d = dst + row * ld + piece;
+        E *d = dst + row * ld + tid % PPR * PIECE;
 #pragma unroll
-        for (int i = 0; i < N; ++i) st16(d + i * STEP * ld, r[i]);
-        if (rows < C) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (row + i * STEP >= rows) st16(d + i * STEP * ld, zero16());
-        }
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(d + i * STEP * ld) = r[i];
     }
 };
 
@@ -309,14 +305,19 @@ __device__ __forceinline__ float gate_value(uint32_t bits, bool is_bf16) {
 // as well, and a difference of two sums stays a number after exp(g) = 0.
 __device__ __forceinline__ double gate_log2(float g) { return fmax((double)g * 1.4426950408889634, -1024.0); }
 
-// x as the sum of three bf16 numbers.
-struct Split3 { bf16 hi, mid, lo; };
-__device__ __forceinline__ Split3 split3(float x) {
-    Split3 s;
-    s.hi = static_cast<bf16>(x);
-    const float r1 = x - static_cast<float>(s.hi);
-    s.mid = static_cast<bf16>(r1);
-    s.lo = static_cast<bf16>(r1 - static_cast<float>(s.mid));
+// Two numbers as sums of N bf16 pairs, largest first.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int N> struct SplitPair { bf16x2 part[N]; };
+template <int N> __device__ __forceinline__ SplitPair<N> split_pair(float a, float b) {
+    SplitPair<N> s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s.part[i] = __builtin_convertvector((f32x2){a, b}, bf16x2);
+        const uint32_t w = __builtin_bit_cast(uint32_t, s.part[i]);
+        a -= __builtin_bit_cast(float, w << 16);
+        b -= __builtin_bit_cast(float, w & 0xffff0000u);
+    }
     return s;
 }
 
@@ -370,17 +371,17 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
     const size_t ldk = (size_t)w.hk * DK, ldv = (size_t)hv * DV;
     LinStage<E, DK, C, THREADS> rq, rk;
     LinStage<E, DV, C, THREADS> rv;
-    rq.init(ldk, tid);
-    rk.init(ldk, tid);
-    rv.init(ldv, tid);
+    const uint32_t k_bytes = (uint32_t)(ldk * sizeof(E)), v_bytes = (uint32_t)(ldv * sizeof(E));
     uint32_t rg = 0;  // the gate's bits: converting them here would wait for the load
-    auto load = [&](int t0) {
-        const int rows = min(it.hi - t0, C);
-        if constexpr (kOut) rq.load(q + (size_t)t0 * ldk, ldk, rows, tid);
-        rk.load(k + (size_t)t0 * ldk, ldk, rows, tid);
-        rv.load(v + (size_t)t0 * ldv, ldv, rows, tid);
+    auto load_q = [&](int t0) {
+        if constexpr (kOut) rq.load(q + (size_t)t0 * ldk, k_bytes, it.hi - t0, tid);
+    };
+    auto load_k = [&](int t0) { rk.load(k + (size_t)t0 * ldk, k_bytes, it.hi - t0, tid); };
+    auto load_v = [&](int t0) {
+        rv.load(v + (size_t)t0 * ldv, v_bytes, it.hi - t0, tid);
         if (wave == NW - 1) {
-            const size_t ga = (size_t)(t0 + min(lane, rows - 1)) * io.gate_ld + h;
+            const int rows = min(it.hi - t0, C);
+            const size_t ga = (size_t)(t0 + min(lane, rows - 1)) * io.gate_ld + (h >> io.gate_shift);
             rg = io.gate_bf16 ? ((const uint16_t *)io.g)[ga] : ((const uint32_t *)io.g)[ga];
         }
     };
@@ -400,12 +401,16 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
             if (lane == 0) s_total = __builtin_amdgcn_exp2f((float)total);
             decay += total;
         }
-        if constexpr (kOut) rq.store(s_q, LDK, rows, tid);
-        rk.store(s_k, LDK, rows, tid);
-        rv.store(s_v, LDV, rows, tid);
+        if constexpr (kOut) rq.store(s_q, LDK, tid);
+        rk.store(s_k, LDK, tid);
+        rv.store(s_v, LDV, tid);
     };
     // The first chunk's loads go out before the state's: they are waited for first.
-    if (it.lo < it.hi) load(it.lo);
+    if (it.lo < it.hi) {
+        load_q(it.lo);
+        load_k(it.lo);
+        load_v(it.lo);
+    }
 
     // This lane's part of the state: tile (mt, nt) holds dk dk_of(mt) .. + 3 of
     // column dv_of(nt). Two tiles' columns alternate in fours, so that a
@@ -435,8 +440,14 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
     if (it.lo < it.hi) stage(it.lo);
     for (int t0 = it.lo; t0 < it.hi; t0 += C) {
         const bool more = t0 + C < it.hi;
-        if (more) load(t0 + C);
+        // The next chunk's loads are spread over the step, so that no wave
+        // stands in the way of its own products with all of them at once.
+        if (!kOut && more) {
+            load_k(t0 + C);
+            load_v(t0 + C);
+        }
         __syncthreads();
+        if (kOut && more) load_q(t0 + C);
 
         // ---- step 1
         int lane_ = lane0;
@@ -448,6 +459,7 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
             fv[t] = col_frag<OT>(s_v, LDV, t / NT, dv0 + 4 * (t % NT), kVStride, lane);
 
         f32x4 o[kOut ? TT * NT : 1];
+        float gam[TT];  // of the tokens of this lane's output columns
         if constexpr (kOut) {
             // Scores P^T = K Q^T, tiles (tokens j, tokens i). A product's
             // contraction steps reach kStep tiles, past the diagonal too:
@@ -494,63 +506,72 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
                     store4<E>(s_p + i * LDP + frag_pos<OT>(j0), p[s]);
                 }
             }
+#pragma unroll
+            for (int I = 0; I < TT; ++I) gam[I] = s_gamma[16 * I + m];
             GDN_SCHED_BARRIER();
+        }
+        if (kOut && more) load_k(t0 + C);
+        // delta V of contraction step tb, for the state
+        typename OT::Frag vd[2][NT][kParts];
+        auto weigh = [&](int tb, typename OT::Frag (&x)[NT][kParts]) {
+#pragma unroll
+            for (int u = 0; u < OT::KPL / 4; ++u) {
+                const f32x4 d = *reinterpret_cast<const f32x4 *>(s_delta + tb * OT::KW + 16 * u + g4);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float x0 = d[e] * to_f32(fv[tb * NT + nt][4 * u + e]),
+                                    x1 = d[e + 1] * to_f32(fv[tb * NT + nt][4 * u + e + 1]);
+                        if constexpr (kBf16) {
+                            const SplitPair<kParts> s = split_pair<kParts>(x0, x1);
+#pragma unroll
+                            for (int i = 0; i < kParts; ++i) {
+                                x[nt][i][4 * u + e] = s.part[i][0];
+                                x[nt][i][4 * u + e + 1] = s.part[i][1];
+                            }
+                        } else {
+                            x[nt][0][4 * u + e] = x0;
+                            x[nt][0][4 * u + e + 1] = x1;
+                        }
+                    }
+            }
+        };
+        const bool carry = kMode != kLinSegOut || more;
+        if constexpr (kOut) {
+            typename OK::Frag fs[NT * KB];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                f32x4 col[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) col[mt] = S[mt * NT + nt];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) fs[nt * KB + kb] = acc_frag<OK, E>(col, kb);
+            }
 #pragma unroll
             for (int t = 0; t < TT * NT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                if (kb % 2 == 0) GDN_SCHED_BARRIER();
-                typename OK::Frag fs[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    f32x4 col[MT];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) col[mt] = S[mt * NT + nt];
-                    fs[nt] = acc_frag<OK, E>(col, kb);
-                }
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int I = 0; I < TT; ++I) {
                     const typename OK::Frag fq = row_frag<OK>(s_q, LDK, 16 * I, kb, lane);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] = OK::mma(fs[nt], fq, o[I * NT + nt]);
+                    for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] = OK::mma(fs[nt * KB + kb], fq, o[I * NT + nt]);
                 }
-            }
-#pragma unroll
-            for (int I = 0; I < TT; ++I) {
-                const float gamma = s_gamma[16 * I + m];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] *= gamma;
-            }
         }
-
-        GDN_SCHED_BARRIER();
-        if (kMode != kLinSegOut || more) {
-            // S^T <- gamma_C S^T + K^T (delta V)
+        weigh(0, vd[0]);
+        {
             const float total = s_total;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) S[t] *= total;
+        }
+        GDN_SCHED_BARRIER();
+
+        if (kOut && more) load_v(t0 + C);
+        if (carry) {
+            // S^T <- gamma_C S^T + K^T (delta V)
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
-                GDN_SCHED_BARRIER();
-                typename OT::Frag vd[NT][kParts];
-#pragma unroll
-                for (int u = 0; u < OT::KPL / 4; ++u) {
-                    const f32x4 d = *reinterpret_cast<const f32x4 *>(s_delta + tb * OT::KW + 16 * u + g4);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x = d[e] * to_f32(fv[tb * NT + nt][4 * u + e]);
-                            if constexpr (kBf16) {
-                                const Split3 s = split3(x);
-                                vd[nt][0][4 * u + e] = s.hi;
-                                vd[nt][1][4 * u + e] = s.mid;
-                                if constexpr (kParts == 3) vd[nt][2][4 * u + e] = s.lo;
-                            } else {
-                                vd[nt][0][4 * u + e] = x;
-                            }
-                        }
-                }
                 // Two tiles of dk at a time, so that a product does not follow
                 // on the one it adds to.
                 constexpr int kSide = MT < 2 ? 1 : 2;
@@ -566,8 +587,10 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
                         for (int s = 0; s < kSide; ++s)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                S[(mt + s) * NT + nt] = OT::mma(fk[s], vd[nt][part], S[(mt + s) * NT + nt]);
+                                S[(mt + s) * NT + nt] = OT::mma(fk[s], vd[tb & 1][nt][part], S[(mt + s) * NT + nt]);
                 }
+                if (tb + 1 < TB) weigh(tb + 1, vd[(tb + 1) & 1]);
+                GDN_SCHED_BARRIER();
             }
         }
         __syncthreads();
@@ -575,6 +598,12 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
         // ---- step 2
         if constexpr (kOut) {
             constexpr int kStep = OT::KW / 16;
+#pragma unroll
+            for (int I = 0; I < TT; ++I) {
+                const float gamma = gam[I];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) o[I * NT + nt] *= gamma;
+            }
 #pragma unroll
             for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -588,21 +617,29 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
         if (more) stage(t0 + C);
         GDN_SCHED_BARRIER();
         if constexpr (kOut) {
-            E *dst = (E *)io.out + (size_t)t0 * ldv + (size_t)h * DV + dv0 + kVStride * g;
+            const __amdgpu_buffer_rsrc_t rsrc = chunk_rows((E *)io.out + (size_t)t0 * ldv + (size_t)h * DV, v_bytes,
+                                                           min(it.hi - t0, C), DV * (uint32_t)sizeof(E));
+            const uint32_t at = (uint32_t)m * v_bytes + (uint32_t)((dv0 + kVStride * g) * (int)sizeof(E));
 #pragma unroll
-            for (int I = 0; I < TT; ++I)
-                if (16 * I + m < it.hi - t0) {
-                    E *row = dst + (size_t)(16 * I + m) * ldv;
-                    if constexpr (kBf16 && NT == 2) {
-                        bf16x8 x;
+            for (int I = 0; I < TT; ++I) {
+                const int off = (int)(at + (uint32_t)(16 * I) * v_bytes);
+                if constexpr (kBf16) {
+                    bf16x4 x[NT];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = static_cast<bf16>(o[I * NT + (e >> 2)][e & 3]);
-                        *reinterpret_cast<bf16x8 *>(row) = x;
-                    } else {
+                    for (int e = 0; e < 4 * NT; ++e) x[e / 4][e & 3] = static_cast<bf16>(o[I * NT + e / 4][e & 3]);
+                    if constexpr (NT == 2)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            __builtin_bit_cast(u32x4, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7)),
+                            rsrc, off, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x[0]), rsrc, off, 0, 0);
+                } else {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) store4<E>(row + 4 * nt, o[I * NT + nt]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[I * NT + nt]), rsrc,
+                                                               off + 16 * nt, 0, 0);
                 }
+            }
         }
     }
 

@@ -17,11 +17,15 @@ typedef float InstElem;
 
 template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinPrefillArgs &A, hipStream_t st) {
     typedef LinShape<E, DK, DV> SH;
-    const uint32_t hk = (uint32_t)A.hk, group = (uint32_t)(A.hv / A.hk);
+    // The rows of a state are independent, so that one of dv rows is also
+    // 2^dv_shift heads of DV rows with the same gates, whose v, out and states
+    // lie as they do.
+    const int32_t hv = A.hv << A.plan.dv_shift;
+    const uint32_t hk = (uint32_t)A.hk, group = (uint32_t)(hv / A.hk);
     const LinWork w{A.cu, A.num_seqs, (int32_t)A.total_tokens, A.plan.seg_shift, hk, group,
                     (uint32_t)A.plan.items * hk};
     LinIo io;
-    io.q = A.q; io.k = A.k; io.v = A.v; io.g = A.g; io.gate_ld = A.gate_per_head ? 0 : A.hv;
+    io.q = A.q; io.k = A.k; io.v = A.v; io.g = A.g; io.gate_ld = A.gate_per_head ? 0 : A.hv; io.gate_shift = A.plan.dv_shift;
     io.s0 = A.s0; io.s_final = A.s_final; io.out = A.out; io.scale = A.scale;
     io.gate_bf16 = A.gate_bf16; io.state_bf16 = A.state_bf16;
     io.seg_state = reinterpret_cast<float *>(A.ws + A.plan.off_state);
@@ -33,14 +37,14 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
     if (w.seg_shift < 0) return launch(kLinOut, std::integral_constant<LinMode, kLinWhole>());
     hipError_t e = launch(kLinState, std::integral_constant<LinMode, kLinSegState>());
     if (e != hipSuccess) return e;
-    const unsigned blocks = (unsigned)A.num_seqs * (unsigned)A.hv * ((DK * DV / 4 + 255) / 256);
+    const unsigned blocks = (unsigned)A.num_seqs * (unsigned)hv * ((DK * DV / 4 + 255) / 256);
     e = launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV>, dim3(blocks), dim3(256), 0, st, w, io);
     if (e != hipSuccess) return e;
     return launch(kLinOut, std::integral_constant<LinMode, kLinSegOut>());
 }
 
 template <> hipError_t launch_linattn_chunk_k<GDN_INST_BF16, GDN_INST_DK>(const LinPrefillArgs &A, hipStream_t st) {
-    switch (A.dv) {
+    switch (A.dv >> A.plan.dv_shift) {
     case 16: return launch_linattn_chunk<InstElem, GDN_INST_DK, 16>(A, st);
     case 32: return launch_linattn_chunk<InstElem, GDN_INST_DK, 32>(A, st);
     case 64: return launch_linattn_chunk<InstElem, GDN_INST_DK, 64>(A, st);
