@@ -30,8 +30,8 @@ Entry points (same names as the C ABI, without the ``gdn_`` prefix):
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Dict, Optional, Tuple
@@ -75,6 +75,8 @@ def lib_path() -> str:
 def load():
     """Load libgdn.so (built by ``python -m gated_deltanet_linear_02_amd.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -386,17 +388,61 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     return out
 
 
-@contextlib.contextmanager
-def _on_stream(device: torch.device, stream):
-    """The call's device made current (the null stream means the current
-    device's), and its stream torch's current one, so that what is allocated
-    for the call belongs to the stream that uses it."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+# The calls below are short next to their own checks, which are therefore kept
+# lean: one pass over a tensor for its pointer, device and layout.
+
+def _arg(name: str, t: Optional[torch.Tensor], device: int) -> Optional[int]:
+    """The pointer of a tensor that the call's GPU can use (``_on_device`` and
+    ``_ptr`` in one)."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}" if device >= 0 else
+                         f"{name} is on {t.device}, expected a GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, as all tensors passed to libgdn")
+    return t.data_ptr() or None
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a GPU")
+    return t.get_device()
+
+
+def _launch(device: int, stream, call) -> None:
+    """``call(stream handle)`` with the call's device current (the null stream
+    means the current device's), on `stream` or torch's current one."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        handle = stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        _check(call(handle or None))
+    else:
+        with torch.cuda.device(device):
+            _check(call(handle or None))
+
+
+def _empty(shape: tuple, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
+    """Memory for the call: of the stream that uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+
+
+def _shaped(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype) -> None:
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        _expect(name, t, shape, dtype)
+
+
+def _state_dtype(name: str, t: torch.Tensor) -> int:
+    if t.dtype == torch.float32:
+        return GDN_F32
+    if t.dtype == torch.bfloat16:
+        return GDN_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16")
 
 
 def _indices(name: str, t: Optional[torch.Tensor], n: int) -> None:
@@ -405,23 +451,23 @@ def _indices(name: str, t: Optional[torch.Tensor], n: int) -> None:
         raise TypeError(f"{name} must be int32")
 
 
-def _state_dtype(name: str, t: torch.Tensor) -> None:
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name} must be float32 or bfloat16")
-
-
 def _linattn_inputs(q, k, v, g) -> Tuple[int, int, int, int, int, int]:
-    """Shapes and types that both linear-attention calls share; (rows, hk,
-    hv, dk, dv, 1 if g is one gate per head)."""
+    """Shapes and types that both linear-attention calls share: tokens, hk,
+    hv, dk, dv, 1 if g is one gate per head."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q and v must be [tokens, heads, size]")
     n, hk, dk = q.shape
-    hv, dv = v.shape[1], v.shape[2]
-    _expect("k", k, (n, hk, dk), q.dtype)
-    _expect("v", v, (n, hv, dv), q.dtype)
+    _, hv, dv = v.shape
+    _shaped("k", k, (n, hk, dk), q.dtype)
+    _shaped("v", v, (n, hv, dv), q.dtype)
     per_head = g.dim() == 1
-    _expect("g", g, (hv,) if per_head else (n, hv))
+    _shaped("g", g, (hv,) if per_head else (n, hv), g.dtype)
     return n, hk, hv, dk, dv, int(per_head)
+
+
+@functools.lru_cache(maxsize=1024)
+def _linattn_workspace(*sizes: int) -> int:
+    return int(load().gdn_linattn_prefill_workspace_size(*sizes))
 
 
 def linattn_prefill_workspace_size(num_seqs: int, total_tokens: int, hk: int, hv: int, dk: int, dv: int,
@@ -429,8 +475,7 @@ def linattn_prefill_workspace_size(num_seqs: int, total_tokens: int, hk: int, hv
                                    max_seqlen: Optional[int] = None) -> int:
     """Bytes of workspace that ``linattn_prefill`` needs for these sizes; 256
     where it needs none, 0 if the sizes are rejected."""
-    return int(load().gdn_linattn_prefill_workspace_size(num_seqs, total_tokens, int(max_seqlen or 0), hk, hv, dk,
-                                                         dv, _dtype_code(io_dtype)))
+    return _linattn_workspace(num_seqs, total_tokens, int(max_seqlen or 0), hk, hv, dk, dv, _dtype_code(io_dtype))
 
 
 def linattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -456,32 +501,32 @@ def linattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
         raise TypeError("cu_seqlens must be a 1-d int32 tensor")
     N = cu_seqlens.numel() - 1
     io, gate = _dtype_code(q.dtype), _dtype_code(g.dtype)
-    _expect("out", out, (T, hv, dv), q.dtype)
+    _shaped("out", out, (T, hv, dv), q.dtype)
+    states = (N, hv, dv, dk)
+    sdt = state_dtype
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
-        _expect(name, t, (N, hv, dv, dk))
-    given = {t.dtype for t in (initial_state, final_state) if t is not None}
-    if len(given) > 1:
-        raise TypeError("initial_state and final_state must have one dtype")
-    sdt = given.pop() if given else (state_dtype or torch.float32)
-    if state_dtype is not None and sdt != state_dtype:
-        raise TypeError(f"state tensors are {sdt}, state_dtype says {state_dtype}")
+        if t is not None:
+            _shaped(name, t, states, t.dtype)
+            if sdt is not None and t.dtype != sdt:
+                raise TypeError(f"initial_state, final_state and state_dtype must have one dtype: {name} is "
+                                f"{t.dtype}, not {sdt}")
+            sdt = t.dtype
+    sdt = sdt or torch.float32
     hint = int(max_seqlen or 0)
-    dev = q.device
-    _on_device(dev, q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state,
-               final_state=final_state, out=out, workspace=workspace)
-    with _on_stream(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, hv, dv), dtype=q.dtype, device=dev)
-        if final_state is None and write_final_state:
-            final_state = torch.empty((N, hv, dv, dk), dtype=sdt, device=dev)
-        if workspace is None:
-            need = linattn_prefill_workspace_size(N, T, hk, hv, dk, dv, q.dtype, hint)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 256 else None
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(load().gdn_linattn_prefill(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, hint, hk, hv, dk, dv, float(scale), io,
-            gate, per_head, _ptr(initial_state), _ptr(final_state), _dtype_code(sdt), _ptr(out), _ptr(workspace),
-            ws_bytes, st.cuda_stream or None))
+    dev = _device_of("q", q)
+    if out is None:
+        out = _empty((T, hv, dv), q.dtype, dev, stream)
+    if final_state is None and write_final_state:
+        final_state = _empty(states, sdt, dev, stream)
+    if workspace is None:
+        need = _linattn_workspace(N, T, hint, hk, hv, dk, dv, io)
+        if need > 256:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+    args = (_arg("q", q, dev), _arg("k", k, dev), _arg("v", v, dev), _arg("g", g, dev),
+            _arg("cu_seqlens", cu_seqlens, dev), N, T, hint, hk, hv, dk, dv, scale, io, gate, per_head,
+            _arg("initial_state", initial_state, dev), _arg("final_state", final_state, dev), _dtype_code(sdt),
+            _arg("out", out, dev), _arg("workspace", workspace, dev), 0 if workspace is None else workspace.nbytes)
+    _launch(dev, stream, lambda st: load().gdn_linattn_prefill(*args, st))
     return out, final_state
 
 
@@ -496,20 +541,20 @@ def linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     ``state_out`` (a second pool like ``state``), written to the same slots
     there while ``state`` stays as it is. No gradient is recorded."""
     B, hk, hv, dk, dv, per_head = _linattn_inputs(q, k, v, g)
-    _state_dtype("state", state)
-    _expect("state", state, (state.shape[0], hv, dv, dk))
-    _expect("state_out", state_out, tuple(state.shape), state.dtype)
-    _expect("out", out, (B, hv, dv), q.dtype)
+    sdt = _state_dtype("state", state)
+    pool = state.shape[0]
+    _shaped("state", state, (pool, hv, dv, dk), state.dtype)
+    _shaped("state_out", state_out, (pool, hv, dv, dk), state.dtype)
+    _shaped("out", out, (B, hv, dv), q.dtype)
     _indices("state_slots", state_slots, B)
-    dev = q.device
-    _on_device(dev, q=q, k=k, v=v, g=g, state=state, state_out=state_out, state_slots=state_slots, out=out)
-    with _on_stream(dev, stream) as st:
-        if out is None:
-            out = torch.empty((B, hv, dv), dtype=q.dtype, device=dev)
-        _check(load().gdn_linattn_decode_step(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), B, hk, hv, dk, dv, float(scale), _dtype_code(q.dtype),
-            _dtype_code(g.dtype), per_head, _ptr(state), _ptr(state_out), _dtype_code(state.dtype),
-            _ptr(state_slots), state.shape[0], _ptr(out), st.cuda_stream or None))
+    dev = _device_of("q", q)
+    if out is None:
+        out = _empty((B, hv, dv), q.dtype, dev, stream)
+    args = (_arg("q", q, dev), _arg("k", k, dev), _arg("v", v, dev), _arg("g", g, dev), B, hk, hv, dk, dv, scale,
+            _dtype_code(q.dtype), _dtype_code(g.dtype), per_head, _arg("state", state, dev),
+            _arg("state_out", state_out, dev), sdt, _arg("state_slots", state_slots, dev), pool,
+            _arg("out", out, dev))
+    _launch(dev, stream, lambda st: load().gdn_linattn_decode_step(*args, st))
     return out
 
 
@@ -517,20 +562,24 @@ GDN_I8, GDN_E4M3 = 0, 1
 
 
 def _state_cache(state, cache, scales, slots, entries) -> tuple:
-    """Checks that both state-cache calls share; the sizes and types they pass on."""
-    _state_dtype("state", state)
+    """Checks that both state-cache calls share; the device, and what they
+    pass on: state, its type, slots, pool; cache, code, scales, entries, size; sizes."""
+    sdt = _state_dtype("state", state)
     if state.dim() != 4 or cache.dim() != 4:
         raise ValueError("state and cache must be [states, hv, dv, dk]")
     if cache.dtype not in (torch.int8, torch.float8_e4m3fn):
         raise TypeError("cache must be int8 or float8_e4m3fn")
-    hv, dv, dk = state.shape[1:]
-    _expect("cache", cache, (cache.shape[0], hv, dv, dk))
-    _expect("scales", scales, (cache.shape[0], hv, dv), torch.float32)
-    n = next((t.numel() for t in (slots, entries) if t is not None), min(state.shape[0], cache.shape[0]))
+    pool, hv, dv, dk = state.shape
+    size = cache.shape[0]
+    _shaped("cache", cache, (size, hv, dv, dk), cache.dtype)
+    _shaped("scales", scales, (size, hv, dv), torch.float32)
+    n = slots.numel() if slots is not None else entries.numel() if entries is not None else min(pool, size)
     _indices("slots", slots, n)
     _indices("entries", entries, n)
-    _on_device(state.device, state=state, cache=cache, scales=scales, slots=slots, entries=entries)
-    return n, hv, dk, dv, GDN_I8 if cache.dtype == torch.int8 else GDN_E4M3
+    dev = _device_of("state", state)
+    return (dev, (_arg("state", state, dev), sdt, _arg("slots", slots, dev), pool),
+            (_arg("cache", cache, dev), GDN_I8 if cache.dtype == torch.int8 else GDN_E4M3,
+             _arg("scales", scales, dev), _arg("entries", entries, dev), size), (n, hv, dk, dv))
 
 
 def state_cache_write(state: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, *,
@@ -542,11 +591,8 @@ def state_cache_write(state: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     ``entries[i]``, one scale per row of dk values. slots, entries int32 [n] on
     the device; None counts 0, 1, ... (n from the other one, or with both
     None as many as both pools hold)."""
-    n, hv, dk, dv, code = _state_cache(state, cache, scales, slots, entries)
-    with _on_stream(state.device, stream) as st:
-        _check(load().gdn_state_cache_write(
-            _ptr(state), _dtype_code(state.dtype), _ptr(slots), state.shape[0], _ptr(cache), code, _ptr(scales),
-            _ptr(entries), cache.shape[0], n, hv, dk, dv, st.cuda_stream or None))
+    dev, s, c, sizes = _state_cache(state, cache, scales, slots, entries)
+    _launch(dev, stream, lambda st: load().gdn_state_cache_write(*s, *c, *sizes, st))
 
 
 def state_cache_read(cache: torch.Tensor, scales: torch.Tensor, state: torch.Tensor, *,
@@ -556,11 +602,8 @@ def state_cache_read(cache: torch.Tensor, scales: torch.Tensor, state: torch.Ten
     (``gdn_state_cache_read``): ``state[slots[i]] = cache[entries[i]] *
     scales[entries[i]]``; arguments as ``state_cache_write``. One entry may go
     to many slots."""
-    n, hv, dk, dv, code = _state_cache(state, cache, scales, slots, entries)
-    with _on_stream(state.device, stream) as st:
-        _check(load().gdn_state_cache_read(
-            _ptr(cache), code, _ptr(scales), _ptr(entries), cache.shape[0], _ptr(state), _dtype_code(state.dtype),
-            _ptr(slots), state.shape[0], n, hv, dk, dv, st.cuda_stream or None))
+    dev, s, c, sizes = _state_cache(state, cache, scales, slots, entries)
+    _launch(dev, stream, lambda st: load().gdn_state_cache_read(*c, *s, *sizes, st))
 
 
 # gdn_tune_prefill's candidates in its order: (chunk, state rows per scan
