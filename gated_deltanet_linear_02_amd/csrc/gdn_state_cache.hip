@@ -7,13 +7,14 @@
 // A row that holds a NaN or an infinity gets the scale NaN and codes 0, so
 // that it reads back as NaN; a row of zeros gets the scale 0.
 //
-// The codes are those of the exact quotient. x / scale is first rounded to
-// fp32 (y, by two Newton corrections of x times the rounded reciprocal);
-// where that lands on the middle between two codes, the sign of the remainder
-// x - y scale, which one fused multiply-add gives exactly, moves it off by one
-// unit in the last place to the side that the quotient is on. Middles end in
-// at least 16 zero bits, and a correctly rounded y reaches one only if
-// the quotient is within half a unit of it, so no other y needs moving.
+// The codes are those of the exact quotient. t, x times the rounded reciprocal
+// of the scale, is within 2^-23 of it (relative), so the quotient lies between
+// t (1 - 2^-22) and t (1 + 2^-22), and where both round to the same code that
+// is its code. Else it is next to the middle between the two, and the sign of
+// x - middle * scale, which one fused multiply-add gives exactly, decides: a
+// few values of a million in fp32 states, but bf16 states have many exact ties.
+// Rows of tiny values are lifted (exactly) by 2^64 first, so that reciprocal
+// and remainder are ordinary numbers.
 //
 // Bound by memory: 4 bytes (2 for bf16 states) and 1 byte per value, each
 // touched once. A lane takes one 16-byte piece of a state row and its 4 (8)
@@ -64,20 +65,50 @@ struct CacheWhere {
 
 constexpr float kInt8Top = 127.f, kE4m3Top = 448.f;
 
-// Two codes (int8 or e4m3) at a time would not fill a store: four quotients
-// to four code bytes.
-template <bool kE4m3> __device__ __forceinline__ uint32_t pack_codes(const float (&y)[4]) {
+// Four quotients to four code bytes, to nearest, ties to even. int8: adding
+// 1.5 2^23 rounds to a whole number and leaves it in the low bits. The second
+// form takes t times f, rounded once, and asks for |t f| below 2^21 only.
+template <bool kE4m3> __device__ __forceinline__ uint32_t pack_codes(const float (&t)[4], float f) {
     if constexpr (kE4m3) {
         int w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0] * f, t[1] * f, w, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(t[2] * f, t[3] * f, w, true);
         return (uint32_t)w;
     } else {
-        uint32_t w = 0;
+        uint32_t b[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w |= ((uint32_t)(int)rintf(y[e]) & 255u) << (8 * e);
-        return w;
+        for (int e = 0; e < 4; ++e) b[e] = __builtin_bit_cast(uint32_t, __builtin_fmaf(t[e], f, 12582912.f));
+        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0c);
+        return lo | hi;
     }
+}
+
+template <bool kE4m3> __device__ __forceinline__ void unpack_codes(uint32_t w, float (&c)[4]) {
+    if constexpr (kE4m3) {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+        c[0] = lo[0]; c[1] = lo[1]; c[2] = hi[0]; c[3] = hi[1];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = (float)(int8_t)(w >> (8 * e));
+    }
+}
+
+// Of two neighbouring codes per byte, `lo` nearer to zero, that of x / s.
+template <bool kE4m3> __device__ __forceinline__ uint32_t decide(uint32_t lo, uint32_t hi, const float (&x)[4], float s) {
+    float a[4], b[4];
+    unpack_codes<kE4m3>(lo, a);
+    unpack_codes<kE4m3>(hi, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float rest = __builtin_fmaf(-0.5f * (a[e] + b[e]), s, x[e]);
+        const bool odd = (lo >> (8 * e)) & 1u;
+        const bool take = rest == 0.f ? odd : (rest > 0.f) == (x[e] > 0.f);
+        const uint32_t mask = take ? 255u << (8 * e) : 0u;
+        lo = (lo & ~mask) | (hi & mask);
+    }
+    return lo;
 }
 
 template <typename SE, int DK, bool kE4m3>
@@ -122,31 +153,28 @@ __global__ __launch_bounds__(256) void gdn_state_cache_write_kernel(const SE *__
         // Rounded up, the scale of the largest values would read back as infinity.
         if (scale * kTop == __builtin_inff())
             scale = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, scale) - 1u);
-        // Rows of tiny values are lifted (exactly) so that the reciprocal
-        // and the remainders are ordinary numbers.
-        const float lift = amax < 0x1p-60f ? 0x1p64f : 1.f;
-        const float s = scale * lift;
         const bool some = finite && scale > 0.f;
+        float s = scale;
+        if (amax < 0x1p-60f) {
+            s *= 0x1p64f;
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) x[p][e] *= 0x1p64f;
+        }
         const float inv = some ? 1.f / s : 0.f;
         uint32_t w[EPL / 4];
 #pragma unroll
         for (int m = 0; m < EPL / 4; ++m) {
-            float y[4];
+            float t[4], xm[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float xx = x[p][4 * m + e] * lift;
-                float t = xx * inv;
-                t = __builtin_fmaf(__builtin_fmaf(-t, s, xx), inv, t);
-                t = __builtin_fmaf(__builtin_fmaf(-t, s, xx), inv, t);
-                const float rest = __builtin_fmaf(-t, s, xx);
-                const uint32_t b = __builtin_bit_cast(uint32_t, t);
-                if (rest != 0.f && (b & 0xffffu) == 0u) {
-                    const bool away = (rest > 0.f) == (t > 0.f);  // the quotient's magnitude is the larger
-                    t = __builtin_bit_cast(float, away ? b + 1u : b - 1u);
-                }
-                y[e] = some ? fminf(fmaxf(t, -kTop), kTop) : 0.f;
+                xm[e] = x[p][4 * m + e];
+                // a scale that underflowed may be too small for its row
+                t[e] = fminf(fmaxf(xm[e] * inv, -kTop), kTop);
             }
-            w[m] = pack_codes<kE4m3>(y);
+            const uint32_t lo = pack_codes<kE4m3>(t, 1.f - 0x1p-22f), hi = pack_codes<kE4m3>(t, 1.f + 0x1p-22f);
+            w[m] = lo;
+            if (__any(lo != hi)) w[m] = decide<kE4m3>(lo, hi, xm, s);
+            if (!some) w[m] = 0;
         }
         if (r < where.rows) {
             uint8_t *dst = cache + (to + r) * DK + EPL * lr;
@@ -157,18 +185,6 @@ __global__ __launch_bounds__(256) void gdn_state_cache_write_kernel(const SE *__
             }
             if (lr == 0) scales[to + r] = scale;
         }
-    }
-}
-
-template <bool kE4m3> __device__ __forceinline__ void unpack_codes(uint32_t w, float (&c)[4]) {
-    if constexpr (kE4m3) {
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
-        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-        c[0] = lo[0]; c[1] = lo[1]; c[2] = hi[0]; c[3] = hi[1];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = (float)(int8_t)(w >> (8 * e));
     }
 }
 
