@@ -385,31 +385,40 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
             rg = io.gate_bf16 ? ((const uint16_t *)io.g)[ga] : ((const uint32_t *)io.g)[ga];
         }
     };
-    double decay = 0.0;  // of the whole segment, log 2 (last wave)
+    double decay = 0.0;  // of the chunks staged so far, log 2 (last wave)
     auto stage = [&](int t0) {
         const int rows = min(it.hi - t0, C);
         if (wave == NW - 1) {
             const double c = wave_scan_f64(lane < rows ? gate_log2(gate_value(rg, io.gate_bf16)) : 0.0);
             const double total = lane_f64(c, C - 1);
             if (lane < C) {
-                const float hi = (float)c;
-                s_chi[lane] = hi;
-                s_clo[lane] = (float)(c - (double)hi);
-                s_gamma[lane] = io.scale * __builtin_amdgcn_exp2f((float)c);
-                s_delta[lane] = __builtin_amdgcn_exp2f((float)(total - c));
+                if constexpr (kOut) {
+                    const float hi = (float)c;
+                    s_chi[lane] = hi;
+                    s_clo[lane] = (float)(c - (double)hi);
+                    s_gamma[lane] = io.scale * __builtin_amdgcn_exp2f((float)c);
+                    s_delta[lane] = __builtin_amdgcn_exp2f((float)(total - c));
+                } else {
+                    s_delta[lane] = __builtin_amdgcn_exp2f((float)(decay + (total - c)));
+                }
             }
-            if (lane == 0) s_total = __builtin_amdgcn_exp2f((float)total);
+            if (kOut && lane == 0) s_total = __builtin_amdgcn_exp2f((float)total);
             decay += total;
         }
         if constexpr (kOut) rq.store(s_q, LDK, tid);
         rk.store(s_k, LDK, tid);
         rv.store(s_v, LDV, tid);
     };
+    // kLinSegState needs no state on its way, only the one at the end: it goes
+    // from the last chunk to the first, so that every token's decay to the end of
+    // the segment is known when the token comes, and the sum is never scaled.
+    constexpr int step = kOut ? C : -C;
+    const int first = kOut ? it.lo : it.lo + ((it.hi - it.lo + C - 1) / C - 1) * C;
     // The first chunk's loads go out before the state's: they are waited for first.
     if (it.lo < it.hi) {
-        load_q(it.lo);
-        load_k(it.lo);
-        load_v(it.lo);
+        load_q(first);
+        load_k(first);
+        load_v(first);
     }
 
     // This lane's part of the state: tile (mt, nt) holds dk dk_of(mt) .. + 3 of
@@ -420,34 +429,35 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
     auto dk_of = [&](int t) { return tile_base<OK>(t / NT) + OK::KPL * g; };
     auto dv_of = [&](int t) { return dv0 + kVStride * (m >> 2) + 4 * (t % NT) + (m & 3); };
     f32x4 S[kTiles];
-    const size_t seg_at = ((size_t)item * hv + h) * (DK * DV) + tid * 4;
     const size_t state_at = ((size_t)it.seq * hv + h) * (DK * DV);
+    auto load_initial = [&](int t) {
+        const size_t at = state_at + (size_t)dv_of(t) * DK + dk_of(t);
+        return io.state_bf16 ? load4f<bf16>((const bf16 *)io.s0 + at) : load4f<float>((const float *)io.s0 + at);
+    };
+    const size_t seg_at = ((size_t)item * hv + h) * (DK * DV) + tid * 4;
     if (kOut && it.seg > 0) {
         const float *src = io.seg_state + seg_at - (size_t)hv * (DK * DV);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) S[t] = *reinterpret_cast<const f32x4 *>(src + t * THREADS * 4);
-    } else if (io.s0 && it.seg == 0) {
+    } else if (kOut && io.s0 && it.seg == 0) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            const size_t at = state_at + (size_t)dv_of(t) * DK + dk_of(t);
-            S[t] = io.state_bf16 ? load4f<bf16>((const bf16 *)io.s0 + at) : load4f<float>((const float *)io.s0 + at);
-        }
+        for (int t = 0; t < kTiles; ++t) S[t] = load_initial(t);
     } else {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    if (it.lo < it.hi) stage(it.lo);
-    for (int t0 = it.lo; t0 < it.hi; t0 += C) {
-        const bool more = t0 + C < it.hi;
+    if (it.lo < it.hi) stage(first);
+    for (int t0 = first; kOut ? t0 < it.hi : t0 >= it.lo; t0 += step) {
+        const bool more = kOut ? t0 + C < it.hi : t0 > it.lo;
         // The next chunk's loads are spread over the step, so that no wave
         // stands in the way of its own products with all of them at once.
         if (!kOut && more) {
-            load_k(t0 + C);
-            load_v(t0 + C);
+            load_k(t0 + step);
+            load_v(t0 + step);
         }
         __syncthreads();
-        if (kOut && more) load_q(t0 + C);
+        if (kOut && more) load_q(t0 + step);
 
         // ---- step 1
         int lane_ = lane0;
@@ -510,7 +520,7 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
             for (int I = 0; I < TT; ++I) gam[I] = s_gamma[16 * I + m];
             GDN_SCHED_BARRIER();
         }
-        if (kOut && more) load_k(t0 + C);
+        if (kOut && more) load_k(t0 + step);
         // delta V of contraction step tb, for the state
         typename OT::Frag vd[2][NT][kParts];
         auto weigh = [&](int tb, typename OT::Frag (&x)[NT][kParts]) {
@@ -560,14 +570,14 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
                 }
         }
         weigh(0, vd[0]);
-        {
+        if constexpr (kOut) {
             const float total = s_total;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) S[t] *= total;
         }
         GDN_SCHED_BARRIER();
 
-        if (kOut && more) load_v(t0 + C);
+        if (kOut && more) load_v(t0 + step);
         if (carry) {
             // S^T <- gamma_C S^T + K^T (delta V)
 #pragma unroll
@@ -614,7 +624,7 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
                 }
         }
         GDN_SCHED_BARRIER();
-        if (more) stage(t0 + C);
+        if (more) stage(t0 + step);
         GDN_SCHED_BARRIER();
         if constexpr (kOut) {
             const __amdgpu_buffer_rsrc_t rsrc = chunk_rows((E *)io.out + (size_t)t0 * ldv + (size_t)h * DV, v_bytes,
@@ -644,6 +654,17 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
     }
 
     if constexpr (kMode == kLinSegState) {
+        if (io.s0 && it.seg == 0) {
+            if (tid == THREADS - 64) s_total = __builtin_amdgcn_exp2f((float)decay);
+            __syncthreads();
+            const float total = s_total;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const f32x4 x = load_initial(t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[t][e] = __builtin_fmaf(total, x[e], S[t][e]);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4 *>(io.seg_state + seg_at + t * THREADS * 4) = S[t];
         if (tid == THREADS - 64) io.seg_decay[(size_t)item * hv + h] = __builtin_amdgcn_exp2f((float)decay);
