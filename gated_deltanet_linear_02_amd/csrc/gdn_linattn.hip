@@ -182,21 +182,26 @@ hipError_t launch_linattn_decode(const LinDecodeArgs &A, hipStream_t st) {
 // rounds of two per compute unit; one takes a fixed time and one per chunk of
 // its segment, less with a unit to itself. States of 128 rows may go as two of
 // 64: half the work per workgroup, but the scores are formed twice. Segments cost
-// a pass for their states, the joining (memory, and a chain over a sequence's
-// segments) and two more launches. Fitted at HK = 16, HV = 32, d = 128 and 64 to
-// 1 x 512 .. 16,384 and 8 x 512 tokens; measured there (all kernels, us):
-//   1 x 512     two of 64 rows: whole 26.4, segments of 128: 27.3, of 64: 27.9
-//   1 x 1,024   two of 64: segments of 128 33.1, of 256 34.2; one: of 128 38.2
-//   1 x 2,048   two of 64: of 256 44.0; one: of 256 49.3
-//   1 x 4,096   two of 64: of 512 63.9; one: of 256 66.2, of 512 70.5
-//   1 x 16,384  one: of 1,024 174, of 512 195; two of 64: of 1,024 202
-//   8 x 512     one: whole 39.7, of 256 75.4; two of 64: whole 41.4
+// a pass for their states, and their states one of two ways: summed by every
+// workgroup for itself, a chain over the segments before it, which is less for
+// few segments; or by the join kernel, a launch and one pass over the states.
+// Fitted at HK = 16, HV = 32, d = 128 to 1 x 512 .. 16,384 and to eight sequences
+// of 62,064 tokens in all; measured there (all kernels, us; "+" with the join):
+//   1 x 256     two of 64 rows: whole 15.9; segments of 128: 17.9
+//   1 x 512     two of 64: of 128 20.1, 26.4+; whole 26.0; one: of 128 26.3
+//   1 x 1,024   two of 64: of 128 26.5, 30.3+, of 256 29.1, 32.7+
+//   1 x 2,048   two of 64: of 256 35.1, 41.4+; one: of 256 42.6, 43.9+
+//   1 x 4,096   two of 64: of 512 56.2, 61.4+; one: of 256 60.0, of 512 59.8
+//   1 x 16,384  one: of 1,024 163, 161+, of 512 179+; two of 64: of 1,024 193+
+//   8: 62,064   one: of 2,048 606, 603+, of 1,024 629, 625+, of 4,096 665
+//   8 x 512     one: whole 39.6, of 256 62.2; two of 64: whole 41.4
+// and at HK = 2, HV = 4, 16,001 tokens: two of 64: of 256 62.8, 44.6+.
 LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv,
                      bool io_bf16) {
     const double chunk = io_bf16 ? 64 : 32, cus = 256;
     const double N = (double)num_seqs, T = (double)total_tokens;
     // Without a hint the longest sequence may be all there is.
-    const double longest = max_seqlen ? (double)max_seqlen : T, mean = T / N;
+    const double longest = max_seqlen ? (double)max_seqlen : T;
     LinPlan best;
     double best_t = 0;
     auto consider = [&](int32_t dv_shift, int32_t seg_shift) {
@@ -204,29 +209,41 @@ LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
         const double heads = (double)(hv << dv_shift);
         const bool split = seg_shift >= 0;
         const double L = split ? (double)((int64_t)1 << seg_shift) : 0;
-        const double items = split ? T / L + (num_seqs > 1 ? 0.5 * N : 0) : N;
-        const double wgs = items * heads;
-        // per chunk: outputs, states; with a unit to itself and with a second workgroup
-        const double out1 = wide ? 3.2 : 2.0, out2 = wide ? 5.4 : 3.4, st1 = wide ? 2.0 : 1.3, st2 = wide ? 3.5 : 1.7;
-        const double rounds = std::max(1.0, wgs / (2 * cus));
-        const double full = std::min(1.0, std::max(0.0, wgs / cus - 1.0));  // units with two
-        auto pass = [&](double fixed, double one, double two, double tokens, double most) {
-            const double step = one + full * (two - one);
+        // Sequences end inside their last segment: half a segment more each on
+        // average, one at most.
+        const double items = split ? std::max(N, T / L + (num_seqs > 1 ? 0.5 * N : 0)) : N;
+        const double bound = split ? T / L + (num_seqs > 1 ? N : 0) : N;
+        const bool shared = bound * heads > cus;  // units with two
+        auto pass = [&](double fixed, double one, double two, double most) {
+            auto rounds = [&](double n, double tokens) {
+                return std::max(1.0, n * heads / (2 * cus)) *
+                       (fixed + std::max(1.0, tokens / chunk) * (shared ? two : one));
+            };
+            // between even segments and as many full ones as there may be
+            double t = rounds(items, std::min(most, T / items));
+            if (split) t = 0.5 * (t + rounds(bound, most));
             // the longest workgroup may outlast the rounds of the others
-            return std::max(rounds * (fixed + std::ceil(tokens / chunk) * step), fixed + std::ceil(most / chunk) * one);
+            return std::max(t, fixed + std::ceil(most / chunk) * one);
         };
         double t;
+        bool join = false;
         if (split) {
-            const double seg = std::min(L, longest), segs = std::ceil(longest / L);
-            t = pass(9.5, out1, out2, seg, seg) + pass(7.5, st1, st2, seg, seg) + 4 + 4 +
-                items * (double)hv * (double)(dk * dv) * 8 / 6e6 + 0.11 * segs;
+            const double segs = std::ceil(longest / L), tile = (double)(dk * (dv >> dv_shift) * 4);
+            const double states = items * heads * tile;
+            const double chain = std::max(segs * (0.05 + tile * 10e-6), states * (0.5 * items / N + 1) / 15e6);
+            const double joined = 3.7 + states / 3.9e6 + 0.06 * segs;
+            join = joined < chain;
+            t = wide ? pass(7, 2.0, 3.35, std::min(L, longest)) + pass(8, 3.1, 5.1, std::min(L, longest))
+                     : pass(6.5, 1.15, 1.8, std::min(L, longest)) + pass(6.2, 2.35, 3.5, std::min(L, longest));
+            t += std::min(joined, chain) + 1;
         } else {
-            t = pass(9, 1.35 * out1, 1.35 * out2, mean, longest);
+            t = wide ? pass(8, 4.0, 6.5, longest) : pass(6.2, 2.45, 4.4, longest);
         }
         if (best_t == 0 || t < best_t) {
             best_t = t;
             best.dv_shift = dv_shift;
             best.seg_shift = seg_shift;
+            best.join = join;
         }
     };
     for (int32_t f = 0; f <= (dv == 128 ? 1 : 0); ++f) {

@@ -12,6 +12,7 @@ namespace gdn {
 struct LinPlan {
     int32_t seg_shift = -1;
     int32_t dv_shift = 0;       // a state of dv rows goes as 2^dv_shift states of fewer
+    bool join = false;          // segments are joined by a kernel, not by each workgroup for itself
     int64_t items = 0;          // sequences, or the bound on segments
     size_t off_state = 0;       // float [items][hv][dv * dk], accumulator order
     size_t off_decay = 0;       // float [items][hv << dv_shift]

@@ -221,6 +221,7 @@ struct LinIo {
     float *seg_decay;  // [item][hv]
     float scale;
     bool gate_bf16, state_bf16;
+    bool joined;  // the join kernel has run: seg_state holds the states at the ends of the segments
 };
 
 template <typename E, int DK, int DV> struct LinShape {
@@ -435,10 +436,29 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
         return io.state_bf16 ? load4f<bf16>((const bf16 *)io.s0 + at) : load4f<float>((const float *)io.s0 + at);
     };
     const size_t seg_at = ((size_t)item * hv + h) * (DK * DV) + tid * 4;
-    if (kOut && it.seg > 0) {
-        const float *src = io.seg_state + seg_at - (size_t)hv * (DK * DV);
+    // The state at the end of segment seg + n - 1, from the states of the
+    // segments (not joined: a chain over all of them).
+    auto load_segments = [&](int n) {
+        const size_t ld = (size_t)hv * (DK * DV);
+        const float *src = io.seg_state + seg_at + (ptrdiff_t)(io.joined ? n - 1 : -it.seg) * (ptrdiff_t)ld;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) S[t] = *reinterpret_cast<const f32x4 *>(src + t * THREADS * 4);
+        if (io.joined) return;
+        const float *dec = io.seg_decay + (size_t)item * hv + h - (ptrdiff_t)it.seg * hv;
+        for (int s = 1; s < it.seg + n; ++s) {
+            src += ld;
+            dec += hv;
+            const float d = *dec;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(src + t * THREADS * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[t][e] = __builtin_fmaf(d, S[t][e], x[e]);
+            }
+        }
+    };
+    if (kOut && it.seg > 0) {
+        load_segments(0);
     } else if (kOut && io.s0 && it.seg == 0) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) S[t] = load_initial(t);
@@ -669,16 +689,15 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
         for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4 *>(io.seg_state + seg_at + t * THREADS * 4) = S[t];
         if (tid == THREADS - 64) io.seg_decay[(size_t)item * hv + h] = __builtin_amdgcn_exp2f((float)decay);
     } else if (io.s_final && it.seg == 0) {
-        // Split: the joined state of the last segment, stored by the
+        // Split: the state at the end of the last segment, stored by the
         // workgroup that has read the initial state, which may be the same
         // buffer.
-        const float *joined = io.seg_state + seg_at + (size_t)(it.segs - 1) * hv * (DK * DV);
+        if constexpr (kMode == kLinSegOut) load_segments(it.segs);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             const size_t at = state_at + (size_t)dv_of(t) * DK + dk_of(t);
-            const f32x4 x = kMode == kLinWhole ? S[t] : *reinterpret_cast<const f32x4 *>(joined + t * THREADS * 4);
-            if (io.state_bf16) store4<bf16>((bf16 *)io.s_final + at, x);
-            else store4<float>((float *)io.s_final + at, x);
+            if (io.state_bf16) store4<bf16>((bf16 *)io.s_final + at, S[t]);
+            else store4<float>((float *)io.s_final + at, S[t]);
         }
     }
 }

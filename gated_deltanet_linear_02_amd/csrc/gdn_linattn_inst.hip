@@ -30,6 +30,7 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
     io.gate_bf16 = A.gate_bf16; io.state_bf16 = A.state_bf16;
     io.seg_state = reinterpret_cast<float *>(A.ws + A.plan.off_state);
     io.seg_decay = reinterpret_cast<float *>(A.ws + A.plan.off_decay);
+    io.joined = A.plan.join;
     const dim3 grid((unsigned)lin_grid(w.units, group)), block(SH::THREADS);
     auto launch = [&](KernelKind kind, auto mode) {
         return launch_kernel(kind, gdn_linattn_chunk_kernel<E, DK, DV, mode()>, grid, block, 0, st, w, io);
@@ -37,9 +38,11 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
     if (w.seg_shift < 0) return launch(kLinOut, std::integral_constant<LinMode, kLinWhole>());
     hipError_t e = launch(kLinState, std::integral_constant<LinMode, kLinSegState>());
     if (e != hipSuccess) return e;
-    const unsigned blocks = (unsigned)A.num_seqs * (unsigned)hv * ((DK * DV / 4 + 255) / 256);
-    e = launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV>, dim3(blocks), dim3(256), 0, st, w, io);
-    if (e != hipSuccess) return e;
+    if (io.joined) {
+        const unsigned blocks = (unsigned)A.num_seqs * (unsigned)hv * ((DK * DV / 4 + 255) / 256);
+        e = launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV>, dim3(blocks), dim3(256), 0, st, w, io);
+        if (e != hipSuccess) return e;
+    }
     return launch(kLinOut, std::integral_constant<LinMode, kLinSegOut>());
 }
 
