@@ -147,10 +147,12 @@ template <typename F> static hipError_t with_types(bool io_bf16, bool gate_bf16,
     return gate_bf16 ? f(float(), bf16(), float()) : f(float(), float(), float());
 }
 
-int32_t linattn_decode_slices(int32_t dk, int32_t dv, bool state_bf16) {
+int32_t linattn_decode_lanes(int32_t dk, int32_t dv, bool state_bf16) {
     int32_t n = 0;
     (void)with_heads(dk, dv, [&](auto kc, auto vc) {
-        n = state_bf16 ? LinDecodeShape<bf16, kc(), vc()>::SLICES : LinDecodeShape<float, kc(), vc()>::SLICES;
+        typedef LinDecodeShape<bf16, kc(), vc()> B;
+        typedef LinDecodeShape<float, kc(), vc()> F;
+        n = state_bf16 ? B::SLICES * B::THREADS : F::SLICES * F::THREADS;
         return hipSuccess;
     });
     return n;
@@ -196,8 +198,8 @@ hipError_t launch_linattn_decode(const LinDecodeArgs &A, hipStream_t st) {
 //   8: 62,064   one: of 2,048 606, 603+, of 1,024 629, 625+, of 4,096 665
 //   8 x 512     one: whole 39.6, of 256 62.2; two of 64: whole 41.4
 // and at HK = 2, HV = 4, 16,001 tokens: two of 64: of 256 62.8, 44.6+.
-LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv,
-                     bool io_bf16) {
+LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hk, int64_t hv, int64_t dk,
+                     int64_t dv, bool io_bf16) {
     const double chunk = io_bf16 ? 64 : 32, cus = 256;
     const double N = (double)num_seqs, T = (double)total_tokens;
     // Without a hint the longest sequence may be all there is.
@@ -209,6 +211,11 @@ LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
         const double heads = (double)(hv << dv_shift);
         const bool split = seg_shift >= 0;
         const double L = split ? (double)((int64_t)1 << seg_shift) : 0;
+        // The grids (launch_linattn_chunk): items x heads, rounded up to whole
+        // turns over the XCDs, and up to 16 workgroups of the join per head.
+        const double most_items = (split ? (double)(total_tokens >> seg_shift) : 0) + N;
+        if (!launchable((most_items * hk + 7) * (heads / hk) * 256) || (split && !launchable(N * hv * 16 * 256)))
+            return;
         // Sequences end inside their last segment: half a segment more each on
         // average, one at most.
         const double items = split ? std::max(N, T / L + (num_seqs > 1 ? 0.5 * N : 0)) : N;
@@ -251,7 +258,7 @@ LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
         for (int32_t s = 6; ((int64_t)1 << s) < total_tokens && s < 31; ++s) consider(f, s);
     }
     LinPlan P = best;
-    P.items = num_seqs;
+    P.items = best_t > 0 ? num_seqs : 0;
     if (P.seg_shift >= 0) {
         P.items = (total_tokens >> P.seg_shift) + num_seqs;
         P.off_state = 0;

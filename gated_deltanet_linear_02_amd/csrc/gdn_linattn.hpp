@@ -7,19 +7,22 @@
 
 namespace gdn {
 
+// A launch has fewer than 2^32 lanes.
+inline bool launchable(double lanes) { return lanes <= (double)UINT32_MAX; }
+
 // How a prefill is split: whole sequences (seg_shift < 0), or segments of
 // 2^seg_shift tokens whose states go through the workspace.
 struct LinPlan {
     int32_t seg_shift = -1;
     int32_t dv_shift = 0;       // a state of dv rows goes as 2^dv_shift states of fewer
     bool join = false;          // segments are joined by a kernel, not by each workgroup for itself
-    int64_t items = 0;          // sequences, or the bound on segments
+    int64_t items = 0;          // sequences, or the bound on segments; 0: too many to launch
     size_t off_state = 0;       // float [items][hv][dv * dk], accumulator order
     size_t off_decay = 0;       // float [items][hv << dv_shift]
     size_t total = 0;           // bytes of workspace
 };
-LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hv, int64_t dk, int64_t dv,
-                     bool io_bf16);
+LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hk, int64_t hv, int64_t dk,
+                     int64_t dv, bool io_bf16);
 
 struct LinPrefillArgs {
     const void *q, *k, *v, *g;
@@ -53,8 +56,8 @@ struct LinDecodeArgs {
 };
 hipError_t launch_linattn_decode(const LinDecodeArgs &a, hipStream_t st);
 
-// Workgroups per (sequence, value head) that launch_linattn_decode takes.
-int32_t linattn_decode_slices(int32_t dk, int32_t dv, bool state_bf16);
+// Lanes per (sequence, value head) that launch_linattn_decode takes.
+int32_t linattn_decode_lanes(int32_t dk, int32_t dv, bool state_bf16);
 
 struct StateCacheArgs {
     void *state;            // written by a read, read by a write

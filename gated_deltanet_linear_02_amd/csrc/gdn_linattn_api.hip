@@ -29,12 +29,10 @@ static int32_t check_linattn_prefill(int32_t num_seqs, int64_t total_tokens, int
     if (max_seqlen != 0 &&
         (max_seqlen < 0 || max_seqlen > total_tokens || max_seqlen * (int64_t)num_seqs < total_tokens))
         return GDN_ERR_BAD_VALUE;
-    // A chunk's rows lie within 32 bits of each other (LinStage).
-    // The grids: items (segments, or sequences) x heads, 64 workgroups of the
-    // join per (sequence, head) at most.
-    const int64_t items = total_tokens / 64 + num_seqs + 8;
-    if ((int64_t)hv * dv > (int64_t)1 << 22 || (int64_t)hk * dk > (int64_t)1 << 22) return GDN_ERR_UNSUPPORTED;
-    if ((double)items * hv > INT32_MAX || (double)num_seqs * hv * 64 > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    // A chunk's rows lie within 32 bits of each other (LinStage), and no sum
+    // of a token's number and a chunk passes an int.
+    if ((int64_t)hv * dv > (int64_t)1 << 22 || (int64_t)hk * dk > (int64_t)1 << 22 || total_tokens > INT32_MAX - 64)
+        return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -45,7 +43,8 @@ size_t gdn_linattn_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens
     if (check_linattn_prefill(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv, io_dtype, GDN_F32, 0, GDN_F32) !=
         GDN_OK)
         return 0;
-    return std::max<size_t>(256, linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv, io_dtype == GDN_BF16).total);
+    const LinPlan plan = linattn_plan(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv, io_dtype == GDN_BF16);
+    return plan.items ? std::max<size_t>(256, plan.total) : 0;
 }
 
 int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const void *g, const int32_t *cu_seqlens,
@@ -56,12 +55,13 @@ int32_t gdn_linattn_prefill(const void *q, const void *k, const void *v, const v
     const int32_t sc = check_linattn_prefill(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv, io_dtype,
                                              gate_dtype, gate_per_head, state_dtype);
     if (sc != GDN_OK) return sc;
+    const LinPlan plan = linattn_plan(num_seqs, total_tokens, max_seqlen, hk, hv, dk, dv, io_dtype == GDN_BF16);
+    if (plan.items == 0) return GDN_ERR_UNSUPPORTED;
     if (!cu_seqlens) return GDN_ERR_NULL_ARG;
     if (total_tokens > 0 && (!q || !k || !v || !g || !out)) return GDN_ERR_NULL_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(initial_state) ||
         !aligned16(final_state))
         return GDN_ERR_MISALIGNED;
-    const LinPlan plan = linattn_plan(num_seqs, total_tokens, max_seqlen, hv, dk, dv, io_dtype == GDN_BF16);
     const size_t used = plan.total;
     if (used && (!workspace || workspace_bytes < used || (reinterpret_cast<uintptr_t>(workspace) & 255)))
         return GDN_ERR_WORKSPACE;
@@ -104,7 +104,7 @@ int32_t gdn_linattn_decode_step(const void *q, const void *k, const void *v, con
     if (sc != GDN_OK) return sc;
     if (batch == 0) return GDN_OK;
     if (!state_slots && num_slots < batch) return GDN_ERR_BAD_SHAPE;
-    if ((int64_t)batch * hv * linattn_decode_slices(dk, dv, state_dtype == GDN_BF16) > INT32_MAX)
+    if (!launchable((double)batch * hv * linattn_decode_lanes(dk, dv, state_dtype == GDN_BF16)))
         return GDN_ERR_UNSUPPORTED;
     if (!q || !k || !v || !g || !state || !out) return GDN_ERR_NULL_ARG;
     if (!state_out) state_out = state;
@@ -151,7 +151,7 @@ static int32_t state_cache_impl(bool to_cache, void *state, int32_t state_dtype,
     if ((!slots && num_slots < n) || (!entries && num_entries < n)) return GDN_ERR_BAD_SHAPE;
     // A workgroup takes at least 32 rows.
     const int64_t rows = (int64_t)hv * dv;
-    if (rows > INT32_MAX || (rows + 31) / 32 * n > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (rows > INT32_MAX || !launchable((double)((rows + 31) / 32) * n * 256)) return GDN_ERR_UNSUPPORTED;
     if (!state || !cache || !scales) return GDN_ERR_NULL_ARG;
     if (!aligned16(state) || !aligned16(cache)) return GDN_ERR_MISALIGNED;
     const Range r_state = span(state, (size_t)num_slots * rows * dk * dtype_bytes(state_dtype)),

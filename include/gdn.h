@@ -61,7 +61,7 @@ typedef enum {
     GDN_OK = 0,
     GDN_ERR_NULL_ARG = 1,    /* a required pointer is NULL */
     GDN_ERR_BAD_SHAPE = 2,   /* negative size, hv % hk != 0, ... */
-    GDN_ERR_UNSUPPORTED = 3, /* head size, chunk or dtype outside the built set */
+    GDN_ERR_UNSUPPORTED = 3, /* head size, chunk or dtype outside the built set, or a size past a limit */
     GDN_ERR_WORKSPACE = 4,   /* workspace NULL or smaller than required */
     GDN_ERR_HIP = 5,         /* a HIP runtime call or launch failed */
     GDN_ERR_ALIAS = 6,       /* an output or the workspace overlaps another buffer */
@@ -420,6 +420,8 @@ int32_t gdn_tune_cache_load(const char *path, int32_t *entries);
  * - state_dtype GDN_F32 or GDN_BF16 is the element type of the states;
  *   GDN_BF16 needs io_dtype GDN_BF16. The arithmetic on states is fp32 with
  *   either (a prefill rounds the final state once, a decode step the new one).
+ * - At most 2^22 are hk dk and hv dv, 2^31 - 65 total_tokens, and 2^23
+ *   sequences x hv; more may be GDN_ERR_UNSUPPORTED.
  * - k, q, v must be finite: what follows a non-finite value in its sequence
  *   is not defined, nor are the up to 63 tokens before it. Other sequences are
  *   untouched by it.

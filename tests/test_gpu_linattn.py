@@ -97,6 +97,25 @@ def test_prefill_long(lens, hk, hv, d, io, hint):
     run_checked(x, lens, what="long", max_seqlen=max(lens) if hint else None)
 
 
+@pytest.mark.parametrize("io,state", [(BF, F32), (BF, BF), (F32, F32)])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv,kinds", [
+    ([90], 2, 4, 64, 64, "out"),                               # whole
+    ([300], 2, 4, 64, 64, "state out"),                        # segments, each sums those before it
+    ([2048], 4, 16, 128, 128, "state out"),
+    ([700, 1, 1500], 2, 8, 64, 128, "state out"),
+    ([16001], 2, 4, 64, 64, "state join out"),                 # segments joined by a kernel
+    ([9000, 0, 7000, 63], 1, 2, 128, 128, "state join out"),
+])
+def test_prefill_each_way_of_splitting(lens, hk, hv, dk, dv, kinds, io, state):
+    d = make(lens, hk, hv, dk, dv, io, state=state, seed=hv + sum(lens))
+    gdn.timing_start(8)
+    run_checked(d, lens, state=state, what=kinds, max_seqlen=max(lens))
+    ran = [k for k, r in gdn.timing_stop().items() if r["count"]]
+    if io == F32 and lens == [2048]:
+        kinds = "state join out"  # (chunks are half as long)
+    assert ran == [f"linattn_{k}" for k in kinds.split()]
+
+
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("name", ["zero", "reset", "strong", "growing", "constant"])
 def test_prefill_gates(name, io):

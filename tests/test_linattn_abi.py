@@ -57,6 +57,28 @@ def test_prefill_workspace_refusals(lib):  # noqa: F811
         assert _prefill(lib, T=100000, ws=FAKE + 5 * G) == ALIAS
 
 
+@no_gpu
+def test_size_limits(lib):  # noqa: F811
+    """Rows, tokens and launches past what 32 bits address are refused, and
+    nothing below the stated limits is."""
+    size = lib.gdn_linattn_prefill_workspace_size
+    top = (1 << 31) - 65
+    assert size(1, top, 0, 1, 1, 16, 16, BF16) >= 256 and size(1, top + 1, 0, 1, 1, 16, 16, BF16) == 0
+    assert size(1, 64, 0, 1, 1 << 15, 16, 128, BF16) >= 256 and size(1, 64, 0, 1, (1 << 15) + 1, 16, 128, BF16) == 0
+    assert size(1, 64, 0, 1 << 15, 1 << 16, 128, 64, BF16) >= 256
+    assert size(1, 64, 0, 1 << 16, 1 << 16, 128, 64, BF16) == 0
+    for T in (0, 1, 1 << 20, 1 << 23, top):
+        for hk, hv in ((1, 1), (1, 8), (16, 128)):
+            for dk, dv in ((16, 16), (128, 128)):
+                n = (1 << 23) // hv
+                assert size(n, T, 0, hk, hv, dk, dv, BF16) >= 256
+                assert size(4 * n, T, 0, hk, hv, dk, dv, F32) == 0
+    assert _prefill(lib, T=top + 1) == UNSUPPORTED
+    assert _decode(lib, batch=1 << 23) == UNSUPPORTED
+    assert _decode(lib, batch=1 << 21, dk=128, sdt=BF16) == UNSUPPORTED
+    assert _cache(lib, True, n=1 << 23) == UNSUPPORTED
+
+
 def _decode(lib, **kw):
     a = dict(q=FAKE, k=FAKE + G, v=FAKE + 2 * G, g=FAKE + 3 * G, batch=4, hk=2, hv=4, dk=64, dv=128, scale=1.0,
              io=BF16, gate=F32, per_head=0, state=FAKE + 4 * G, state_out=None, sdt=F32, slots=FAKE + 5 * G, pool=8,
