@@ -259,10 +259,15 @@ LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
     }
     LinPlan P = best;
     P.items = best_t > 0 ? num_seqs : 0;
+    if (num_seqs > kLinListed) {
+        P.sorted = true;
+        P.off_cu = 0;
+        P.total = align256(sizeof(int32_t) * ((size_t)num_seqs + 1));
+    }
     if (P.seg_shift >= 0) {
         P.items = (total_tokens >> P.seg_shift) + num_seqs;
-        P.off_state = 0;
-        P.off_decay = align256((size_t)P.items * hv * dk * dv * sizeof(float));
+        P.off_state = P.total;
+        P.off_decay = align256(P.off_state + (size_t)P.items * hv * dk * dv * sizeof(float));
         P.total = align256(P.off_decay + (size_t)P.items * (hv << P.dv_shift) * sizeof(float));
     }
     return P;

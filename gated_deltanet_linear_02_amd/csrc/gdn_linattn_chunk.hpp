@@ -126,6 +126,7 @@ template <typename OP, typename E> __device__ __forceinline__ typename OP::Frag 
 // needs no table, and is less than floor(T / L) + N in all.
 struct LinWork {
     const int32_t *cu;
+    bool sorted;         // cu is in order already (kLinListed)
     int32_t num_seqs, total_tokens, seg_shift;
     uint32_t hk, group;  // query/key heads, value heads on each
     uint32_t units;      // items x hk
@@ -153,13 +154,34 @@ __device__ __forceinline__ int wave_scan_max(int x) {
     return x;
 }
 
+// The sequence of an item where the offsets are in order: the last n whose
+// first item, floor(start / L) + n, is not behind it. 64 candidates at a time.
+__device__ __forceinline__ int lin_search(const LinWork &w, int item, int lane) {
+    if (w.seg_shift < 0) return item;
+    int from = 0, len = w.num_seqs;
+    for (;;) {
+        const int step = (len + 63) >> 6, n = from + lane * step;
+        const uint64_t at = __ballot(lane * step < len && (w.cu[min(n, w.num_seqs)] >> w.seg_shift) + n <= item);
+        if (!at) return -1;  // (in the first turn only)
+        const int l = 63 - __builtin_clzll(at);
+        from += l * step;
+        len = min(step, len - l * step);
+        if (step == 1) return from;
+    }
+}
+
 // Each wave finds its workgroup's item. Offsets are clamped into [0, T] and
-// made non-decreasing (a running maximum), 64 sequences at a time.
+// made non-decreasing (a running maximum), 64 sequences at a time; many
+// sequences have it done before (gdn_linattn_offsets_kernel).
 __device__ __forceinline__ LinItem lin_item(const LinWork &w, int item, int lane) {
     auto clampT = [&](int x) { return min(max(x, 0), w.total_tokens); };
     int carry = clampT(w.cu[0]);  // where sequence `base` starts
     int lo = 0, hi = 0, seq = -1;
-    for (int base = 0; base < w.num_seqs; base += 64) {
+    if (w.sorted) {
+        seq = __builtin_amdgcn_readfirstlane(lin_search(w, item, lane));
+        lo = w.cu[max(seq, 0)];
+        hi = w.cu[max(seq, 0) + 1];
+    } else for (int base = 0; base < w.num_seqs; base += 64) {
         const int n = base + lane;
         int e = n < w.num_seqs ? clampT(w.cu[n + 1]) : 0;
         e = wave_scan_max(max(e, carry));        // where sequence n ends
@@ -207,6 +229,40 @@ __device__ __forceinline__ bool lin_place(const LinWork &w, uint32_t &item, uint
     return u < w.units;
 }
 inline int64_t lin_grid(int64_t units, int64_t group) { return (units + 7) / 8 * 8 * group; }
+
+// Offsets in order for calls of more sequences than kLinListed, where each
+// workgroup would read many. One workgroup; 4 sequences a lane and turn.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void gdn_linattn_offsets_kernel(const int32_t *__restrict__ cu, int num_seqs,
+                                                                      int total_tokens, int32_t *__restrict__ sorted)
+{
+    __shared__ int s_top[2][THREADS / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto clampT = [&](int x) { return min(max(x, 0), total_tokens); };
+    int carry = clampT(cu[0]), turn = 0;
+    if (tid == 0) sorted[0] = carry;
+    for (int base = 0; base < num_seqs; base += 4 * THREADS, turn ^= 1) {
+        const int n = base + 4 * tid;
+        int e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = n + j < num_seqs ? clampT(cu[n + j + 1]) : 0;
+#pragma unroll
+        for (int j = 1; j < 4; ++j) e[j] = max(e[j], e[j - 1]);
+        const int upto = wave_scan_max(e[3]);
+        const int before = __builtin_amdgcn_update_dpp(0, upto, 0x138, 0xf, 0xf, false);  // wave_shr 1
+        if (lane == 63) s_top[turn][wave] = upto;
+        __syncthreads();
+        int start = max(carry, lane == 0 ? 0 : before);
+        for (int i = 0; i < THREADS / 64; ++i) {
+            const int top = s_top[turn][i];
+            if (i < wave) start = max(start, top);
+            carry = max(carry, top);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < num_seqs) sorted[n + j + 1] = max(e[j], start);
+    }
+}
 
 // ------------------------------------------------------------- the kernel
 
@@ -715,8 +771,8 @@ __global__ __launch_bounds__(256) void gdn_linattn_join_kernel(LinWork w, LinIo 
     const int n = nh / hv, h = nh - n * hv;
     // the sequence's bounds, as lin_item finds them
     auto clampT = [&](int x) { return min(max(x, 0), w.total_tokens); };
-    int lo = clampT(w.cu[0]), hi = lo;
-    for (int j = lane; j <= n; j += 64) {
+    int lo = clampT(w.cu[w.sorted ? n : 0]), hi = lo;
+    for (int j = w.sorted ? n : lane; j <= n; j += 64) {
         const int e = clampT(w.cu[j + 1]);
         hi = max(hi, e);
         if (j < n) lo = max(lo, e);

@@ -22,8 +22,16 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
     // lie as they do.
     const int32_t hv = A.hv << A.plan.dv_shift;
     const uint32_t hk = (uint32_t)A.hk, group = (uint32_t)(hv / A.hk);
-    const LinWork w{A.cu, A.num_seqs, (int32_t)A.total_tokens, A.plan.seg_shift, hk, group,
-                    (uint32_t)A.plan.items * hk};
+    LinWork w{A.cu, A.plan.sorted, A.num_seqs, (int32_t)A.total_tokens, A.plan.seg_shift, hk, group,
+              (uint32_t)A.plan.items * hk};
+    hipError_t e = hipSuccess;
+    if (w.sorted) {
+        int32_t *cu = reinterpret_cast<int32_t *>(A.ws + A.plan.off_cu);
+        e = launch_kernel(kSchedule, gdn_linattn_offsets_kernel<1024>, dim3(1), dim3(1024), 0, st, A.cu, A.num_seqs,
+                          (int32_t)A.total_tokens, cu);
+        if (e != hipSuccess) return e;
+        w.cu = cu;
+    }
     LinIo io;
     io.q = A.q; io.k = A.k; io.v = A.v; io.g = A.g; io.gate_ld = A.gate_per_head ? 0 : A.hv; io.gate_shift = A.plan.dv_shift;
     io.s0 = A.s0; io.s_final = A.s_final; io.out = A.out; io.scale = A.scale;
@@ -36,7 +44,7 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
         return launch_kernel(kind, gdn_linattn_chunk_kernel<E, DK, DV, mode()>, grid, block, 0, st, w, io);
     };
     if (w.seg_shift < 0) return launch(kLinOut, std::integral_constant<LinMode, kLinWhole>());
-    hipError_t e = launch(kLinState, std::integral_constant<LinMode, kLinSegState>());
+    e = launch(kLinState, std::integral_constant<LinMode, kLinSegState>());
     if (e != hipSuccess) return e;
     if (io.joined) {
         const unsigned blocks = (unsigned)A.num_seqs * (unsigned)hv * ((DK * DV / 4 + 255) / 256);

@@ -172,6 +172,43 @@ def test_prefill_malformed_offsets_are_made_monotone():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("lens,hk,hv,d,kinds", [
+    ([i % 4 for i in range(5000)], 1, 1, 16, ["schedule", "linattn_out"]),
+    ([7] * 300 + [6000] + [0, 1, 64, 65] * 40, 1, 2, 64, ["schedule", "linattn_state", "linattn_out"]),
+    ([0] * 399 + [500], 1, 2, 32, ["linattn_out"]),
+    ([500] + [0] * 400, 1, 2, 32, ["schedule", "linattn_out"]),
+], ids=["short", "one_long", "at_the_limit", "past_the_limit"])
+def test_prefill_many_sequences(lens, hk, hv, d, kinds):
+    x = make(lens, hk, hv, d, d, BF, seed=len(lens), extra=5)
+    gdn.timing_start(8)
+    run_checked(x, lens, what="many sequences", max_seqlen=max(lens), start=5)
+    ran = [k for k, r in gdn.timing_stop().items() if r["count"] and k != "linattn_join"]
+    assert ran == kinds
+
+
+@pytest.mark.parametrize("long", [0, 4000])
+def test_prefill_malformed_offsets_of_many_sequences(long):
+    """Offsets that jump ahead, fall back and leave [0, T], against the running
+    maximum of what they are clamped to."""
+    N, T = 700, 2100 + long
+    gen = torch.Generator().manual_seed(long)
+    bad = (torch.arange(N + 1) * 3 + torch.randint(-40, 40, (N + 1,), generator=gen)).to(torch.int32)
+    bad[450:] += long
+    bad[-5:] = torch.tensor([T + 7, 2 ** 31 - 1, -2 ** 31, 0, T])
+    good = bad.clamp(0, T).cummax(0).values.to(torch.int32)
+    d = make([T], 1, 2, 32, 64, BF, init=False, seed=9)
+    note("malformed cu_seqlens of many sequences")
+    a = gdn.linattn_prefill(d["q"], d["k"], d["v"], d["g"], bad.cuda())
+    b = gdn.linattn_prefill(d["q"], d["k"], d["v"], d["g"], good.cuda())
+    torch.cuda.synchronize()
+    first = int(good[0])
+    assert torch.equal(a[0][first:], b[0][first:]) and torch.equal(a[1], b[1])
+    w_o, w_S, mag, A = ref.scan(d["q"], d["k"], d["v"], d["g"], good.diff().tolist(), start=first)
+    t_o, t_S = ref.prefill_bounds(w_o, w_S, mag, A, BF, F32, T, 32)
+    ref.check(a[0][first:], w_o[first:], t_o[first:], "out")
+    ref.check(a[1], w_S, t_S, "state")
+
+
 @pytest.mark.parametrize("io,state", [(BF, F32), (BF, BF), (F32, F32)])
 def test_prefill_in_place_state_and_repeat(io, state):
     lens = [2500, 33]
