@@ -23,7 +23,10 @@ namespace gdn {
 // is spread over LPR = DK / 8 lanes (StateLane), every lane group takes
 // NRL rows of its workgroup, and q.S, k.q are summed over the lanes of a row
 // by DPP moves. Loads and stores of fp32 states are nontemporal (nothing reads
-// them again before the next step).
+// them again before the next step). 64 sequences, 32 heads, d = 128: fp32 states
+// 42.7 us (6.3 TB/s), bf16 states 22.8 us (5.9 TB/s); one sequence 4.3 us.
+// Threads and rows per lane group, same sizes: fp32 256 and 1 42.7 us, 1,024 and
+// 2 44.0; bf16 256 and 1 26.9, 512 and 2 24.8, 1,024 and 2 22.8.
 template <typename SE> constexpr int kLinDecodeThreads = 256;
 template <> constexpr int kLinDecodeThreads<bf16> = 1024;
 template <typename SE> constexpr int kLinDecodeRowsPerLane = 1;
