@@ -172,6 +172,35 @@ def test_prefill_malformed_offsets_are_made_monotone():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("io", [BF, F32])
+def test_prefill_widest_rows(io):
+    """hv dv = 2^22, the limit: rows of a block 16 MB (fp32) apart."""
+    d = make([40, 9], 1, 1 << 15, 16, 128, io, seed=8)
+    run_checked(d, [40, 9], what="widest rows")
+
+
+@pytest.mark.parametrize("lens", [[150, 131], [3000]])
+def test_prefill_past_32_bits(lens):
+    """The last tokens of tensors of more than 2^31 elements."""
+    T, hk, hv, dk, dv = (1 << 31) // (32 * 128) + 4000, 1, 32, 16, 128
+    n = sum(lens)
+    d = make(lens, hk, hv, dk, dv, BF, seed=n)
+    big = {x: torch.zeros((T, *d[x].shape[1:]), dtype=d[x].dtype, device="cuda") for x in ("q", "k", "v", "g")}
+    for x in big:
+        big[x][T - n:] = d[x]
+    out = torch.zeros_like(big["v"])
+    cu = d["cu"] + (T - n)
+    note(f"linattn_prefill {tuple(out.shape)} lens={lens}")
+    o, f = gdn.linattn_prefill(big["q"], big["k"], big["v"], big["g"], cu, scale=0.7, initial_state=d["init"], out=out,
+                               max_seqlen=None)
+    torch.cuda.synchronize()
+    w_o, w_S, mag, A = ref.scan(d["q"], d["k"], d["v"], d["g"], lens, scale=0.7, init=d["init"])
+    t_o, t_S = ref.prefill_bounds(w_o, w_S, mag, A, BF, F32, max(lens), dk)
+    ref.check(o[T - n:], w_o, t_o, "out")
+    ref.check(f, w_S, t_S, "state")
+    assert not o[:T - n].any()
+
+
 @pytest.mark.parametrize("lens,hk,hv,d,kinds", [
     ([i % 4 for i in range(5000)], 1, 1, 16, ["schedule", "linattn_out"]),
     ([7] * 300 + [6000] + [0, 1, 64, 65] * 40, 1, 2, 64, ["schedule", "linattn_state", "linattn_out"]),
@@ -380,6 +409,11 @@ def test_decode_second_pool_and_skipped_slots(state):
     again = gdn.linattn_decode_step(d["q"], d["k"], d["v"], d["g"], d["state"], scale=0.7, state_slots=slots)
     used = slots[[0, 2, 3, 5]].long()
     assert torch.equal(again, out) and torch.equal(d["state"][used], second[used])
+
+
+def test_decode_pool_beyond_32_bits():
+    d = decode_inputs(3, 16, 32, 128, 128, BF, F32, BF, False, 4200, 5)
+    decode_checked(d, torch.tensor([4199, 0, 4097], dtype=torch.int32, device="cuda"))
 
 
 def test_decode_forgets_at_minus_infinity():
