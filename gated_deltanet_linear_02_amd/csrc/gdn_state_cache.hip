@@ -20,10 +20,11 @@
 // touched once. A lane takes one 16-byte piece of a state row and its 4 (8)
 // codes, LPR = dk / EPL lanes a row, so that every load and store of a wave is
 // contiguous; NR rows per lane group keep several loads in flight. 64 states of
-// 32 heads, 128 x 128, int8 or e4m3: fp32 written in 32 us (5.2 TB/s), read back
-// in 24.5 (6.9); bf16 22.8 (4.5) and 15.5 (6.5). A write does some 15 operations
-// a value beside its memory; deciding near-ties apart, with both neighbouring
-// codes formed, took fp32 states 30.6 us and bf16 states 25.4.
+// 32 heads, 128 x 128, int8 or e4m3: fp32 written in 31.4 us (5.4 TB/s), read back
+// in 24.5 (6.9); bf16 22.5 (4.5) and 15.4 (6.6). NR = 1, 2, 4, 8: fp32 written in
+// 34.3, 32.9, 31.4, 32.0, bf16 read in 18.9, 15.6, 15.4, 15.7. A write does some
+// 19 operations a value beside its memory; deciding near-ties apart, with both
+// neighbouring codes formed, took fp32 states 30.6 us and bf16 states 25.4.
 #include "gdn_linattn.hpp"
 #include "gdn_rows.hpp"
 
@@ -69,9 +70,9 @@ struct CacheWhere {
 
 constexpr float kInt8Top = 127.f, kE4m3Top = 448.f;
 
-// x / s, rounded to odd; inv is 1 / s to fp32's precision.
+// x / s, rounded to odd; inv is 1 / s to a step or so.
 __device__ __forceinline__ float quotient_odd(float x, float s, float inv) {
-    const float t = x * inv;                                  // within two steps
+    const float t = x * inv;                                  // within three steps
     const float q = __builtin_fmaf(__builtin_fmaf(-t, s, x), inv, t);  // within one
     const float rest = __builtin_fmaf(-q, s, x);
     uint32_t b = __builtin_bit_cast(uint32_t, q);
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(256) void gdn_state_cache_write_kernel(const SE *__
 #pragma unroll
             for (int e = 0; e < EPL; ++e) x[p][e] *= 0x1p64f;
         }
-        const float inv = some ? 1.f / s : 0.f;
+        const float inv = some ? __builtin_amdgcn_rcpf(s) : 0.f;
         uint32_t w[EPL / 4];
 #pragma unroll
         for (int m = 0; m < EPL / 4; ++m) {
