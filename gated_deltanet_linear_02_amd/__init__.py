@@ -389,39 +389,49 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
 
 
 # The calls below are short next to their own checks, which are therefore kept
-# lean: one pass over a tensor for its pointer, device and layout.
+# lean: one function per tensor, what went wrong looked for only when it did.
 
-def _arg(name: str, t: Optional[torch.Tensor], device: int) -> Optional[int]:
-    """The pointer of a tensor that the call's GPU can use (``_on_device`` and
-    ``_ptr`` in one)."""
+_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+
+
+def _use(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, device: int) -> Optional[int]:
+    """The pointer of a tensor with the call's sizes, on the call's GPU
+    (``_expect``, ``_on_device`` and ``_ptr`` in one)."""
     if t is None:
         return None
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}" if device >= 0 else
-                         f"{name} is on {t.device}, expected a GPU")
-    if not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _expect(name, t, shape, dtype)
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{device}" if device >= 0 else "a GPU"))
         raise ValueError(f"{name} must be contiguous, as all tensors passed to libgdn")
     return t.data_ptr() or None
 
 
-def _device_of(name: str, t: torch.Tensor) -> int:
-    if not t.is_cuda:
+def _use_indices(name: str, t: Optional[torch.Tensor], n: int, device: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is not torch.int32:
+        _expect(name, t, (n,))
+        raise TypeError(f"{name} must be int32")
+    return _use(name, t, (n,), torch.int32, device)
+
+
+def _on_gpu(name: str, t: torch.Tensor, device: int) -> None:
+    if device < 0 or not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected a GPU")
-    return t.get_device()
 
 
-def _launch(device: int, stream, call) -> None:
-    """``call(stream handle)`` with the call's device current (the null stream
-    means the current device's), on `stream` or torch's current one."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        handle = stream.cuda_stream
+def _launch(device: int, stream, call, *args) -> None:
+    """``call(*args, stream handle)`` with the call's device current (the null
+    stream means the current device's), on `stream` or torch's current one."""
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if device == torch._C._cuda_getDevice():
-        _check(call(handle or None))
+        status = call(*args, handle or None)
     else:
         with torch.cuda.device(device):
-            _check(call(handle or None))
+            status = call(*args, handle or None)
+    if status:
+        _check(status)
 
 
 def _empty(shape: tuple, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
@@ -432,37 +442,20 @@ def _empty(shape: tuple, dtype: torch.dtype, device: int, stream) -> torch.Tenso
         return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
 
 
-def _shaped(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype) -> None:
-    if t is not None and (t.shape != shape or t.dtype != dtype):
-        _expect(name, t, shape, dtype)
+def _state_code(name: str, t: torch.Tensor) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return code
 
 
-def _state_dtype(name: str, t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return GDN_F32
-    if t.dtype == torch.bfloat16:
-        return GDN_BF16
-    raise TypeError(f"{name} must be float32 or bfloat16")
-
-
-def _indices(name: str, t: Optional[torch.Tensor], n: int) -> None:
-    _expect(name, t, (n,))
-    if t is not None and t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32")
-
-
-def _linattn_inputs(q, k, v, g) -> Tuple[int, int, int, int, int, int]:
-    """Shapes and types that both linear-attention calls share: tokens, hk,
-    hv, dk, dv, 1 if g is one gate per head."""
-    if q.dim() != 3 or v.dim() != 3:
+def _three(q: torch.Tensor, v: torch.Tensor) -> Tuple[tuple, int, int, int, int, int]:
+    """q's shape and what both linear-attention calls take from q and v:
+    tokens, hk, dk, hv, dv."""
+    shape, v_shape = q.shape, v.shape
+    if len(shape) != 3 or len(v_shape) != 3:
         raise ValueError("q and v must be [tokens, heads, size]")
-    n, hk, dk = q.shape
-    _, hv, dv = v.shape
-    _shaped("k", k, (n, hk, dk), q.dtype)
-    _shaped("v", v, (n, hv, dv), q.dtype)
-    per_head = g.dim() == 1
-    _shaped("g", g, (hv,) if per_head else (n, hv), g.dtype)
-    return n, hk, hv, dk, dv, int(per_head)
+    return (shape, *shape, v_shape[1], v_shape[2])
 
 
 @functools.lru_cache(maxsize=1024)
@@ -496,37 +489,44 @@ def linattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     split. Missing out / final_state / workspace are allocated with torch.
     Returns (out, final_state). No gradient is recorded.
     """
-    T, hk, hv, dk, dv, per_head = _linattn_inputs(q, k, v, g)
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+    shape, T, hk, dk, hv, dv = _three(q, v)
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1:
         raise TypeError("cu_seqlens must be a 1-d int32 tensor")
-    N = cu_seqlens.numel() - 1
-    io, gate = _dtype_code(q.dtype), _dtype_code(g.dtype)
-    _shaped("out", out, (T, hv, dv), q.dtype)
-    states = (N, hv, dv, dk)
+    offsets = cu_seqlens.shape
+    N = offsets[0] - 1
+    dev, dtype, gate, per_head = q.get_device(), q.dtype, g.dtype, g.dim() == 1
+    v_shape, states = (T, hv, dv), (N, hv, dv, dk)
+    p_q, p_k, p_v = _use("q", q, shape, dtype, dev), _use("k", k, shape, dtype, dev), _use("v", v, v_shape, dtype, dev)
+    p_g = _use("g", g, (hv,) if per_head else (T, hv), gate, dev)
+    p_cu, p_out = _use("cu_seqlens", cu_seqlens, offsets, torch.int32, dev), _use("out", out, v_shape, dtype, dev)
+    io, gate = _dtype_code(dtype), _dtype_code(gate)
     sdt = state_dtype
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is not None:
-            _shaped(name, t, states, t.dtype)
-            if sdt is not None and t.dtype != sdt:
+            if sdt is not None and t.dtype is not sdt:
                 raise TypeError(f"initial_state, final_state and state_dtype must have one dtype: {name} is "
                                 f"{t.dtype}, not {sdt}")
             sdt = t.dtype
     sdt = sdt or torch.float32
+    p_init = _use("initial_state", initial_state, states, sdt, dev)
+    p_final = _use("final_state", final_state, states, sdt, dev)
     hint = int(max_seqlen or 0)
-    dev = _device_of("q", q)
+    _on_gpu("q", q, dev)
     if out is None:
-        out = _empty((T, hv, dv), q.dtype, dev, stream)
+        out = _empty(v_shape, dtype, dev, stream)
+        p_out = out.data_ptr() or None
     if final_state is None and write_final_state:
         final_state = _empty(states, sdt, dev, stream)
+        p_final = final_state.data_ptr() or None
     if workspace is None:
         need = _linattn_workspace(N, T, hint, hk, hv, dk, dv, io)
         if need > 256:
             workspace = _empty((need,), torch.uint8, dev, stream)
-    args = (_arg("q", q, dev), _arg("k", k, dev), _arg("v", v, dev), _arg("g", g, dev),
-            _arg("cu_seqlens", cu_seqlens, dev), N, T, hint, hk, hv, dk, dv, scale, io, gate, per_head,
-            _arg("initial_state", initial_state, dev), _arg("final_state", final_state, dev), _dtype_code(sdt),
-            _arg("out", out, dev), _arg("workspace", workspace, dev), 0 if workspace is None else workspace.nbytes)
-    _launch(dev, stream, lambda st: load().gdn_linattn_prefill(*args, st))
+    p_ws, room = None, 0
+    if workspace is not None:
+        p_ws, room = _use("workspace", workspace, workspace.shape, workspace.dtype, dev), workspace.nbytes
+    _launch(dev, stream, (_lib or load()).gdn_linattn_prefill, p_q, p_k, p_v, p_g, p_cu, N, T, hint, hk, hv, dk, dv,
+            scale, io, gate, per_head, p_init, p_final, _dtype_code(sdt), p_out, p_ws, room)
     return out, final_state
 
 
@@ -540,46 +540,48 @@ def linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     int32 [B] on the device or None. The states are updated in place, or, with
     ``state_out`` (a second pool like ``state``), written to the same slots
     there while ``state`` stays as it is. No gradient is recorded."""
-    B, hk, hv, dk, dv, per_head = _linattn_inputs(q, k, v, g)
-    sdt = _state_dtype("state", state)
-    pool = state.shape[0]
-    _shaped("state", state, (pool, hv, dv, dk), state.dtype)
-    _shaped("state_out", state_out, (pool, hv, dv, dk), state.dtype)
-    _shaped("out", out, (B, hv, dv), q.dtype)
-    _indices("state_slots", state_slots, B)
-    dev = _device_of("q", q)
+    shape, B, hk, dk, hv, dv = _three(q, v)
+    dev, dtype, gate, sdt, per_head = q.get_device(), q.dtype, g.dtype, state.dtype, g.dim() == 1
+    code, pool, v_shape = _state_code("state", state), state.shape[0], (B, hv, dv)
+    states = (pool, hv, dv, dk)
+    p_q, p_k, p_v = _use("q", q, shape, dtype, dev), _use("k", k, shape, dtype, dev), _use("v", v, v_shape, dtype, dev)
+    p_g = _use("g", g, (hv,) if per_head else (B, hv), gate, dev)
+    p_old, p_new = _use("state", state, states, sdt, dev), _use("state_out", state_out, states, sdt, dev)
+    p_slots, p_out = _use_indices("state_slots", state_slots, B, dev), _use("out", out, v_shape, dtype, dev)
+    io, gate = _dtype_code(dtype), _dtype_code(gate)
+    _on_gpu("q", q, dev)
     if out is None:
-        out = _empty((B, hv, dv), q.dtype, dev, stream)
-    args = (_arg("q", q, dev), _arg("k", k, dev), _arg("v", v, dev), _arg("g", g, dev), B, hk, hv, dk, dv, scale,
-            _dtype_code(q.dtype), _dtype_code(g.dtype), per_head, _arg("state", state, dev),
-            _arg("state_out", state_out, dev), sdt, _arg("state_slots", state_slots, dev), pool,
-            _arg("out", out, dev))
-    _launch(dev, stream, lambda st: load().gdn_linattn_decode_step(*args, st))
+        out = _empty(v_shape, dtype, dev, stream)
+        p_out = out.data_ptr() or None
+    _launch(dev, stream, (_lib or load()).gdn_linattn_decode_step, p_q, p_k, p_v, p_g, B, hk, hv, dk, dv, scale, io,
+            gate, per_head, p_old, p_new, code, p_slots, pool, p_out)
     return out
 
 
 GDN_I8, GDN_E4M3 = 0, 1
 
 
+_CACHE_CODES = {torch.int8: GDN_I8, torch.float8_e4m3fn: GDN_E4M3}
+
+
 def _state_cache(state, cache, scales, slots, entries) -> tuple:
     """Checks that both state-cache calls share; the device, and what they
     pass on: state, its type, slots, pool; cache, code, scales, entries, size; sizes."""
-    sdt = _state_dtype("state", state)
-    if state.dim() != 4 or cache.dim() != 4:
+    sdt = _state_code("state", state)
+    shape, c_shape, dev = state.shape, cache.shape, state.get_device()
+    if len(shape) != 4 or len(c_shape) != 4:
         raise ValueError("state and cache must be [states, hv, dv, dk]")
-    if cache.dtype not in (torch.int8, torch.float8_e4m3fn):
+    code = _CACHE_CODES.get(cache.dtype)
+    if code is None:
         raise TypeError("cache must be int8 or float8_e4m3fn")
-    pool, hv, dv, dk = state.shape
-    size = cache.shape[0]
-    _shaped("cache", cache, (size, hv, dv, dk), cache.dtype)
-    _shaped("scales", scales, (size, hv, dv), torch.float32)
+    pool, hv, dv, dk = shape
+    size = c_shape[0]
     n = slots.numel() if slots is not None else entries.numel() if entries is not None else min(pool, size)
-    _indices("slots", slots, n)
-    _indices("entries", entries, n)
-    dev = _device_of("state", state)
-    return (dev, (_arg("state", state, dev), sdt, _arg("slots", slots, dev), pool),
-            (_arg("cache", cache, dev), GDN_I8 if cache.dtype == torch.int8 else GDN_E4M3,
-             _arg("scales", scales, dev), _arg("entries", entries, dev), size), (n, hv, dk, dv))
+    s = (_use("state", state, shape, state.dtype, dev), sdt, _use_indices("slots", slots, n, dev), pool)
+    c = (_use("cache", cache, (size, hv, dv, dk), cache.dtype, dev), code,
+         _use("scales", scales, (size, hv, dv), torch.float32, dev), _use_indices("entries", entries, n, dev), size)
+    _on_gpu("state", state, dev)
+    return dev, s, c, (n, hv, dk, dv)
 
 
 def state_cache_write(state: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, *,
@@ -592,7 +594,7 @@ def state_cache_write(state: torch.Tensor, cache: torch.Tensor, scales: torch.Te
     the device; None counts 0, 1, ... (n from the other one, or with both
     None as many as both pools hold)."""
     dev, s, c, sizes = _state_cache(state, cache, scales, slots, entries)
-    _launch(dev, stream, lambda st: load().gdn_state_cache_write(*s, *c, *sizes, st))
+    _launch(dev, stream, (_lib or load()).gdn_state_cache_write, *s, *c, *sizes)
 
 
 def state_cache_read(cache: torch.Tensor, scales: torch.Tensor, state: torch.Tensor, *,
@@ -603,7 +605,7 @@ def state_cache_read(cache: torch.Tensor, scales: torch.Tensor, state: torch.Ten
     scales[entries[i]]``; arguments as ``state_cache_write``. One entry may go
     to many slots."""
     dev, s, c, sizes = _state_cache(state, cache, scales, slots, entries)
-    _launch(dev, stream, lambda st: load().gdn_state_cache_read(*c, *s, *sizes, st))
+    _launch(dev, stream, (_lib or load()).gdn_state_cache_read, *c, *s, *sizes)
 
 
 # gdn_tune_prefill's candidates in its order: (chunk, state rows per scan
