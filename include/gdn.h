@@ -513,7 +513,8 @@ int32_t gdn_state_cache_read(const void *cache, int32_t cache_dtype, const float
  * trace does. gdn_timing_stop() waits for those
  * events, writes for each kernel kind k < n_kinds the number of launches
  * timed (counts[k]) and their summed duration in milliseconds (total_ms[k]),
- * releases the events and stops timing. Kinds: 0 = varlen schedule,
+ * releases the events and stops timing. Kinds: 0 = varlen schedule
+ * (linear attention: offsets put in order),
  * 1 = chunk preparation, 2 = chunk-recurrent scan, 3 = decode step,
  * 4 = token-by-token prefill, 5 = decode step with output normalisation,
  * 6 = output normalisation pass of the prefill, 7, 8, 9 = segment states,
