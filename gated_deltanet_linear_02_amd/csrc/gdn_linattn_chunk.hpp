@@ -776,11 +776,14 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
 // its end, S_s = decay_s S_{s-1} + local_s. One lane per four elements; the
 // chain over segments is a multiply-add each, the loads run ahead of it. Bound by
 // memory, the states read and written once: 34 segments of 32 heads of 128 x 128,
-// 71 MB, take 22 us (6.5 TB/s, some of it from the last-level cache).
-template <int DK, int DV>
-__global__ __launch_bounds__(256) void gdn_linattn_join_kernel(LinWork w, LinIo io)
+// 71 MB, take 22 us (6.5 TB/s, some of it from the last-level cache). Few states
+// leave compute units idle; they go in workgroups of 64 lanes with more loads
+// ahead: 63 segments of 4 heads 10.6 us with 256 and 8, 8.9 with 64 and 16; 118 of
+// 2 heads of 64 x 64 13.9 and 11.1; but 16 of 32 heads 11.9 and 14.9.
+template <int DK, int DV, int THREADS, int kAhead>
+__global__ __launch_bounds__(THREADS) void gdn_linattn_join_kernel(LinWork w, LinIo io)
 {
-    constexpr int kQuads = DK * DV / 4, kBlocks = (kQuads + 255) / 256, kAhead = 8;
+    constexpr int kQuads = DK * DV / 4, kBlocks = (kQuads + THREADS - 1) / THREADS;
     const int lane = threadIdx.x & 63;
     const int hv = (int)(w.hk * w.group);
     const int block = blockIdx.x % kBlocks, nh = blockIdx.x / kBlocks;
@@ -800,7 +803,7 @@ __global__ __launch_bounds__(256) void gdn_linattn_join_kernel(LinWork w, LinIo 
     }
     const int segs = (int)(((uint32_t)(hi - lo) + (1u << w.seg_shift) - 1u) >> w.seg_shift);
     const int item0 = (lo >> w.seg_shift) + n;
-    const int quad = block * 256 + threadIdx.x;
+    const int quad = block * THREADS + threadIdx.x;
     if (quad >= kQuads) return;
     float *at = io.seg_state + ((size_t)item0 * hv + h) * (DK * DV) + (size_t)quad * 4;
     const float *dec = io.seg_decay + (size_t)item0 * hv + h;

@@ -33,7 +33,8 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
         w.cu = cu;
     }
     LinIo io;
-    io.q = A.q; io.k = A.k; io.v = A.v; io.g = A.g; io.gate_ld = A.gate_per_head ? 0 : A.hv; io.gate_shift = A.plan.dv_shift;
+    io.q = A.q; io.k = A.k; io.v = A.v; io.g = A.g;
+    io.gate_ld = A.gate_per_head ? 0 : A.hv; io.gate_shift = A.plan.dv_shift;
     io.s0 = A.s0; io.s_final = A.s_final; io.out = A.out; io.scale = A.scale;
     io.gate_bf16 = A.gate_bf16; io.state_bf16 = A.state_bf16;
     io.seg_state = reinterpret_cast<float *>(A.ws + A.plan.off_state);
@@ -47,8 +48,12 @@ template <typename E, int DK, int DV> hipError_t launch_linattn_chunk(const LinP
     e = launch(kLinState, std::integral_constant<LinMode, kLinSegState>());
     if (e != hipSuccess) return e;
     if (io.joined) {
-        const unsigned blocks = (unsigned)A.num_seqs * (unsigned)hv * ((DK * DV / 4 + 255) / 256);
-        e = launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV>, dim3(blocks), dim3(256), 0, st, w, io);
+        const unsigned heads = (unsigned)A.num_seqs * (unsigned)hv, quads = DK * DV / 4;
+        const unsigned wide = heads * ((quads + 255) / 256);
+        const dim3 few(heads * (quads / 64));
+        e = wide >= 256
+                ? launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV, 256, 8>, dim3(wide), dim3(256), 0, st, w, io)
+                : launch_kernel(kLinJoin, gdn_linattn_join_kernel<DK, DV, 64, 16>, few, dim3(64), 0, st, w, io);
         if (e != hipSuccess) return e;
     }
     return launch(kLinOut, std::integral_constant<LinMode, kLinSegOut>());

@@ -105,6 +105,7 @@ def test_prefill_long(lens, hk, hv, d, io, hint):
     ([700, 1, 1500], 2, 8, 64, 128, "state out"),
     ([16001], 2, 4, 64, 64, "state join out"),                 # segments joined by a kernel
     ([9000, 0, 7000, 63], 1, 2, 128, 128, "state join out"),
+    ([7000], 8, 16, 128, 128, "state join out"),
 ])
 def test_prefill_each_way_of_splitting(lens, hk, hv, dk, dv, kinds, io, state):
     d = make(lens, hk, hv, dk, dv, io, state=state, seed=hv + sum(lens))
