@@ -515,6 +515,8 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
         for (int t = 0; t < kTiles; ++t) S[t] = *reinterpret_cast<const f32x4 *>(src + t * THREADS * 4);
         if (io.joined) return;
         const float *dec = io.seg_decay + (size_t)item * hv + h - (ptrdiff_t)it.seg * hv;
+        // (four segments' loads at once, where there are registers for them)
+#pragma clang loop unroll_count(NT == 1 ? 4 : 1)
         for (int s = 1; s < it.seg + n; ++s) {
             src += ld;
             dec += hv;
@@ -527,7 +529,7 @@ __global__ __launch_bounds__((LinShape<E, DK, DV>::THREADS), (LinShape<E, DK, DV
             }
         }
     };
-    if (kOut && it.seg > 0) {
+    if (kMode == kLinSegOut && it.seg > 0) {
         load_segments(0);
     } else if (kOut && io.s0 && it.seg == 0) {
 #pragma unroll
