@@ -395,8 +395,8 @@ template <int N> __device__ __forceinline__ SplitPair<N> split_pair(float a, flo
 // What a launch computes. kLinWhole: outputs and final states of whole
 // sequences. Split: kLinSegState, the state at the end of each segment as if
 // it began from zero (the first one from the initial state), and its decay;
-// then, joined, kLinSegOut, the outputs from the states before each segment,
-// and the final states. The state that kLinSegOut carries from chunk to chunk
+// then kLinSegOut, the outputs from the states before each segment (joined by
+// the kernel below, or summed by each workgroup), and the final states. The state that kLinSegOut carries from chunk to chunk
 // only goes into outputs, so two parts of delta v, 16 bits, are enough there.
 enum LinMode { kLinWhole, kLinSegState, kLinSegOut };
 
