@@ -396,11 +396,11 @@ template <int N> __device__ __forceinline__ SplitPair<N> split_pair(float a, flo
 // sequences. Split: kLinSegState, the state at the end of each segment as if
 // it began from zero (the first one from the initial state), and its decay;
 // then kLinSegOut, the outputs from the states before each segment (joined by
-// the kernel below, or summed by each workgroup), and the final states. The state that kLinSegOut carries from chunk to chunk
-// only goes into outputs, so two parts of delta v, 16 bits, are enough there.
+// the kernel below, or summed by each workgroup), and the final states. The state
+// that kLinSegOut carries from chunk to chunk only goes into outputs, so two parts
+// of delta v, 16 bits, are enough there.
 enum LinMode { kLinWhole, kLinSegState, kLinSegOut };
 
-//
 // A chunk goes in two steps with a barrier after each, each with as much
 // independent work as there is, for the waves of a CU wait on latencies far
 // more than on any unit:
