@@ -203,7 +203,7 @@ hipError_t launch_linattn_decode(const LinDecodeArgs &A, hipStream_t st) {
 // and at HK = 2, HV = 4, 16,001 tokens: two of 64: of 256 62.8, 44.6+.
 LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen, int64_t hk, int64_t hv, int64_t dk,
                      int64_t dv, bool io_bf16) {
-    const double chunk = io_bf16 ? 64 : 32, cus = 256;
+    const double chunk = io_bf16 ? 64 : 32, xcds = 8, cus = 32;  // compute units of an XCD
     const double N = (double)num_seqs, T = (double)total_tokens;
     // Without a hint the longest sequence may be all there is.
     const double longest = max_seqlen ? (double)max_seqlen : T;
@@ -223,25 +223,30 @@ LinPlan linattn_plan(int64_t num_seqs, int64_t total_tokens, int64_t max_seqlen,
         // average, one at most.
         const double items = split ? std::max(N, T / L + (num_seqs > 1 ? 0.5 * N : 0)) : N;
         const double bound = split ? T / L + (num_seqs > 1 ? N : 0) : N;
-        const bool shared = bound * heads > cus;  // units with two
+        // An XCD takes whole groups of heads that share a key head (lin_place).
+        auto per_xcd = [&](double n) { return std::ceil(n * hk / xcds) * (heads / hk); };
+        const bool shared = per_xcd(bound) > cus;  // units with two
         auto pass = [&](double fixed, double one, double two, double most) {
+            const double step = shared ? two : one;
             auto rounds = [&](double n, double tokens) {
-                return std::max(1.0, n * heads / (2 * cus)) *
-                       (fixed + std::max(1.0, tokens / chunk) * (shared ? two : one));
+                const double r = per_xcd(n) / (2 * cus);
+                return (r > 1 ? r + 0.1 : 1.0) * (fixed + std::max(1.0, tokens / chunk) * step);
             };
             // between even segments and as many full ones as there may be
             double t = rounds(items, std::min(most, T / items));
             if (split) t = 0.5 * (t + rounds(bound, most));
-            // the longest workgroup may outlast the rounds of the others
-            return std::max(t, fixed + std::ceil(most / chunk) * one);
+            // the longest workgroup may outlast the rounds of the others (whole
+            // sequences: in company at first, then alone)
+            return std::max(t, fixed + std::ceil(most / chunk) * (split ? one : 0.5 * (one + step)));
         };
         double t;
         bool join = false;
         if (split) {
             const double segs = std::ceil(longest / L), tile = (double)(dk * (dv >> dv_shift) * 4);
             const double states = items * heads * tile;
-            const double chain = std::max(segs * (0.05 + tile * 10e-6), states * (0.5 * items / N + 1) / 15e6);
-            const double joined = 3.7 + states / 3.9e6 + 0.06 * segs;
+            const double chain = std::max(segs * (wide ? tile * 13e-6 : 0.08 + tile * 4.5e-6),
+                                          states * (0.5 * items / N + 1) / 28e6);
+            const double joined = 3.7 + states / 3.9e6 + 0.055 * segs;
             join = joined < chain;
             t = wide ? pass(7, 2.0, 3.35, std::min(L, longest)) + pass(8, 3.1, 5.1, std::min(L, longest))
                      : pass(6.5, 1.15, 1.8, std::min(L, longest)) + pass(6.2, 2.35, 3.5, std::min(L, longest));
