@@ -30,9 +30,9 @@
 //
 // What bounds it. A chunk of a 128 x 128 state is 64 KB of q, k, v and out
 // and 8.4 MFLOP of products (outputs), so that a long call is bound by
-// memory: 8 sequences of 62,064 tokens, 32 heads, move 1.84 GB in the output
-// pass in 393 us (4.7 TB/s; a large copy reaches 4.95) and 0.99 GB in the state
-// pass in 213 us. A short call is bound by the chain of chunks, 3.1 us each (two
+// memory: 8 sequences of 62,064 tokens, 32 heads, move 2.15 GB in the output
+// pass in 408 us (5.3 TB/s, some of it from the last-level cache; a large copy
+// reaches 4.95) and 1.04 GB in the state pass in 209 us. A short call is bound by the chain of chunks, 3.1 us each (two
 // workgroups on a compute unit 5.1 us each) and by two launches: 4,096 tokens
 // take 20 + 36 us, 29 us of memory. Chunks of 64: with 32 a step took as long
 // and did half as much. Four waves, two workgroups on a compute unit: eight waves
